@@ -59,6 +59,18 @@ SIGNATURES = {
     "bl_graph_destroy": (None, [_p]),
     "bl_forward_norm_grouped_workspace_bytes": (_sz, [_int, _p, _int]),
     "bl_forward_norm_grouped": (_int, [_int, _p, _int, _p, ctypes.c_float, _int, _p, _sz, _p]),
+    "bl_forward_checkpoint_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "bl_forward_checkpoint": (_int, [_p, _int, ctypes.c_float, _i64, _i64, _i64, _p, _p, _int, _p, _p, _p, _p, _p,
+                                     _sz, _p]),
+    "bl_backward_input_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "bl_backward_input": (_int, [_p, _i64, _i64, _i64, _p, _p, _p, _p, _sz, _p]),
+    "bl_backward_weight_workspace_bytes": (_sz, [_i64, _i64, _i64, ctypes.c_uint]),
+    "bl_backward_weight": (_int, [_p, _p, _p, _i64, _i64, _i64, ctypes.c_uint, _p, _p, _sz, _p]),
+    "bl_norm_forward": (_int, [_p, _p, _p, _int, ctypes.c_float, _i64, _i64, _p, _p, _p, _p]),
+    "bl_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "bl_norm_backward": (_int, [_p, _p, _p, _int, ctypes.c_float, _p, _p, _i64, _i64, ctypes.c_uint, _p, _p, _p, _p,
+                                _sz, _p]),
+    "bl_norm_backward_checkpoint": (_int, [_p, _p, _p, _int, ctypes.c_float, _p, _i64, _i64, _p, _p]),
     "bl_matmul_i32_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "bl_matmul_i32": (_int, [_p, _i64, _i64, _i64, _p, _p, _p, _sz, _p]),
     "bl_device_status": (_int, [_int, ctypes.POINTER(_int)]),
@@ -571,6 +583,196 @@ def bl_forward_norm_grouped(problems, norm: int, norm_weights=None, eps: float =
                                          ws.numel() if ws is not None else 0, _stream()),
            "bl_forward_norm_grouped")
     return outs
+
+
+# ---------------------------------------------------------------------------
+# training: checkpointed forward, gradients, the norm and its backward
+# ---------------------------------------------------------------------------
+
+BL_NORM_NONE = 2
+BL_GRAD_ACCUMULATE = 1
+BL_GRAD_BF16 = 2
+
+
+def _train(t: torch.Tensor, dtype, name: str, shape) -> int:
+    """_dev with the shape checked, on the current device (the one whose
+    stream the call uses)."""
+    p = _dev(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return p
+
+
+def _packed(Wp: torch.Tensor, N: int, K: int) -> int:
+    """Packed weights of any shape with the layer's N*K/4 bytes."""
+    p = _dev(Wp, torch.uint8, "Wp")
+    if Wp.numel() != N * K // 4:
+        raise ValueError(f"Wp must hold {N * K // 4} bytes, got {Wp.numel()}")
+    return p
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError(f"{name} must be a matrix")
+    return t.shape
+
+
+def _ws_args(workspace, need: int, device):
+    """(pointer, bytes, tensor kept alive) of a caller's or a new workspace."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _dev(workspace, torch.uint8, "workspace")
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def bl_forward_checkpoint_workspace_bytes(M: int, K: int, N: int, bits: int = 8) -> int:
+    return int(lib().bl_forward_checkpoint_workspace_bytes(M, K, N, bits))
+
+
+def bl_forward_checkpoint(X: torch.Tensor, Wp: torch.Tensor, gamma: torch.Tensor, N: int, bits: int = 8,
+                          norm: int | None = None, eps: float = 1e-5, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None):
+    """bl_forward (norm None), or behind BL_NORM_RMS / BL_NORM_LAYER without
+    parameters, that keeps its activations as 8-bit codes: returns (Y bf16
+    [M, N], Xq int8 [M, K], scale fp32 [M], stat fp32 [M] or None), what
+    bl_backward_weight and bl_norm_backward_checkpoint take."""
+    M, K = _matrix(X, "X")
+    px = _train(X, torch.bfloat16, "X", (M, K))
+    pw = _packed(Wp, N, K)
+    pg = _dev(gamma, torch.float32, "gamma")
+    nrm = BL_NORM_NONE if norm is None else norm
+    Y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+    py = _train(Y, torch.bfloat16, "out", (M, N))
+    Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
+    scale = torch.empty(M, dtype=torch.float32, device=X.device)
+    stat = torch.empty(M, dtype=torch.float32, device=X.device) if nrm != BL_NORM_NONE else None
+    wp, wn, _keep = _ws_args(workspace, lib().bl_forward_checkpoint_workspace_bytes(M, K, N, bits), X.device)
+    _check(lib().bl_forward_checkpoint(px, nrm, eps, M, K, N, pw, pg, bits, py, Xq.data_ptr(), scale.data_ptr(),
+                                       stat.data_ptr() if stat is not None else None, wp, wn, _stream()),
+           "bl_forward_checkpoint")
+    return Y, Xq, scale, stat
+
+
+def bl_backward_input_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().bl_backward_input_workspace_bytes(M, K, N))
+
+
+def bl_backward_input(dY: torch.Tensor, Wp: torch.Tensor, gamma: torch.Tensor, K: int,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """dX = gamma * dY C: bf16 [M, N] output gradients and the packed weights
+    [N, K/4] -> bf16 [M, K]."""
+    M, N = _matrix(dY, "dY")
+    py = _train(dY, torch.bfloat16, "dY", (M, N))
+    pw = _packed(Wp, N, K)
+    pg = _dev(gamma, torch.float32, "gamma")
+    dX = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dY.device)
+    px = _train(dX, torch.bfloat16, "out", (M, K))
+    wp, wn, _keep = _ws_args(workspace, lib().bl_backward_input_workspace_bytes(M, K, N), dY.device)
+    _check(lib().bl_backward_input(py, M, K, N, pw, pg, px, wp, wn, _stream()), "bl_backward_input")
+    return dX
+
+
+def bl_backward_weight_workspace_bytes(M: int, K: int, N: int, flags: int = 0) -> int:
+    return int(lib().bl_backward_weight_workspace_bytes(M, K, N, flags))
+
+
+def bl_backward_weight(dY: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, dtype=torch.float32,
+                       out: torch.Tensor | None = None, accumulate: bool = False,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """dW = dY^T (Xq / scale): bf16 [M, N] output gradients and the forward's
+    int8 codes [M, K] and scales [M] -> fp32 (or bf16) [N, K].  With `out`,
+    its dtype counts; accumulate=True adds to it."""
+    M, N = _matrix(dY, "dY")
+    M2, K = _matrix(Xq, "Xq")
+    py = _train(dY, torch.bfloat16, "dY", (M2, N))
+    pq = _train(Xq, torch.int8, "Xq", (M, K))
+    ps = _train(scale, torch.float32, "scale", (M,))
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((N, K), dtype=dtype, device=dY.device)
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dW must be float32 or bfloat16")
+    po = _train(out, out.dtype, "out", (N, K))
+    flags = (BL_GRAD_ACCUMULATE if accumulate else 0) | (BL_GRAD_BF16 if out.dtype == torch.bfloat16 else 0)
+    wp, wn, _keep = _ws_args(workspace, lib().bl_backward_weight_workspace_bytes(M, K, N, flags), dY.device)
+    _check(lib().bl_backward_weight(py, pq, ps, M, K, N, flags, po, wp, wn, _stream()), "bl_backward_weight")
+    return out
+
+
+def bl_norm_forward(X: torch.Tensor, norm: int, weight: torch.Tensor | None = None,
+                    bias: torch.Tensor | None = None, eps: float = 1e-5, out: torch.Tensor | None = None):
+    """RMSNorm (BL_NORM_RMS) or LayerNorm (BL_NORM_LAYER) of bf16 [M, K] rows:
+    returns (Y bf16 [M, K], mean fp32 [M] or None, stat fp32 [M])."""
+    M, K = _matrix(X, "X")
+    px = _train(X, torch.bfloat16, "X", (M, K))
+    pw = _train(weight, torch.bfloat16, "weight", (K,)) if weight is not None else None
+    pb = _train(bias, torch.bfloat16, "bias", (K,)) if bias is not None else None
+    Y = out if out is not None else torch.empty_like(X)
+    py = _train(Y, torch.bfloat16, "out", (M, K))
+    stat = torch.empty(M, dtype=torch.float32, device=X.device)
+    mean = torch.empty(M, dtype=torch.float32, device=X.device) if norm == BL_NORM_LAYER else None
+    _check(lib().bl_norm_forward(px, pw, pb, norm, eps, M, K, py, mean.data_ptr() if mean is not None else None,
+                                 stat.data_ptr(), _stream()), "bl_norm_forward")
+    return Y, mean, stat
+
+
+def bl_norm_backward_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().bl_norm_backward_workspace_bytes(M, K))
+
+
+def bl_norm_backward(dY: torch.Tensor, X: torch.Tensor, norm: int, stat: torch.Tensor,
+                     mean: torch.Tensor | None = None, weight: torch.Tensor | None = None, need_bias: bool = False,
+                     eps: float = 1e-5, out: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                     dbias: torch.Tensor | None = None, accumulate: bool = False,
+                     workspace: torch.Tensor | None = None):
+    """Gradients of bl_norm_forward: (dX bf16 [M, K], dweight fp32 [K] when
+    there is a weight or `dweight`, dbias fp32 [K] when need_bias or `dbias`).
+    accumulate=True adds to the given dweight and dbias."""
+    M, K = _matrix(X, "X")
+    px = _train(X, torch.bfloat16, "X", (M, K))
+    py = _train(dY, torch.bfloat16, "dY", (M, K))
+    pst = _train(stat, torch.float32, "stat", (M,))
+    pmu = _train(mean, torch.float32, "mean", (M,)) if mean is not None else None
+    pw = _train(weight, torch.bfloat16, "weight", (K,)) if weight is not None else None
+    if accumulate and ((weight is not None and dweight is None) or (need_bias and dbias is None)):
+        raise ValueError("accumulate needs dweight and dbias")
+    if dweight is None and weight is not None:
+        dweight = torch.empty(K, dtype=torch.float32, device=X.device)
+    if dbias is None and need_bias:
+        dbias = torch.empty(K, dtype=torch.float32, device=X.device)
+    pdw = _train(dweight, torch.float32, "dweight", (K,)) if dweight is not None else None
+    pdb = _train(dbias, torch.float32, "dbias", (K,)) if dbias is not None else None
+    dX = out if out is not None else torch.empty_like(X)
+    pdx = _train(dX, torch.bfloat16, "out", (M, K))
+    wp, wn, _keep = None, 0, None
+    if pdw is not None or pdb is not None:
+        wp, wn, _keep = _ws_args(workspace, lib().bl_norm_backward_workspace_bytes(M, K), X.device)
+    _check(lib().bl_norm_backward(py, px, pw, norm, eps, pmu, pst, M, K, BL_GRAD_ACCUMULATE if accumulate else 0, pdx,
+                                  pdw, pdb, wp, wn, _stream()), "bl_norm_backward")
+    return dX, dweight, dbias
+
+
+def bl_norm_backward_checkpoint(dXn: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, norm: int,
+                                stat: torch.Tensor, eps: float = 1e-5,
+                                out: torch.Tensor | None = None) -> torch.Tensor:
+    """Backward of the norm inside bl_forward_checkpoint from its codes: dXn
+    bf16 [M, K] (bl_backward_input), Xq, scale and stat -> dX bf16 [M, K]."""
+    M, K = _matrix(dXn, "dXn")
+    pg = _train(dXn, torch.bfloat16, "dXn", (M, K))
+    pq = _train(Xq, torch.int8, "Xq", (M, K))
+    ps = _train(scale, torch.float32, "scale", (M,))
+    pst = _train(stat, torch.float32, "stat", (M,))
+    dX = out if out is not None else torch.empty_like(dXn)
+    px = _train(dX, torch.bfloat16, "out", (M, K))
+    _check(lib().bl_norm_backward_checkpoint(pg, pq, ps, norm, eps, pst, M, K, px, _stream()),
+           "bl_norm_backward_checkpoint")
+    return dX
 
 
 def bl_matmul_i32(Xq: torch.Tensor, Wp: torch.Tensor, N: int) -> torch.Tensor:

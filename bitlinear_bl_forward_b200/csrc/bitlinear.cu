@@ -24,6 +24,8 @@
 #include "bl_gemm_tc2.cuh"
 #include "bl_gemm_2sm.cuh"
 #include "bl_gemv.cuh"
+#include "bl_grad.cuh"
+#include "bl_norm_grad.cuh"
 #include "bl_decode.cuh"
 #include "bl_probe.cuh"
 #include "bl_weights.cuh"
@@ -1579,10 +1581,305 @@ bl_status bl_forward_norm_grouped(int count, const bl_linear* problems, int norm
   return BL_OK;
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Training: checkpointed forward, gradients, the norm and its backward.
+// ---------------------------------------------------------------------------
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bl_status check_rows(int64_t M, int64_t K) {
+  if (K <= 0 || (K % 64) != 0 || K > kMaxK) return BL_ERR_SHAPE;
+  return check_m(M, K);
+}
+
+// N*K, M*K and M*N below 2^40.
+bl_status check_mnk(int64_t M, int64_t N, int64_t K) {
+  bl_status st = check_shape_nk(N, K);
+  if (st != BL_OK) return st;
+  if (N > INT32_MAX) return BL_ERR_SHAPE;
+  if ((st = check_m(M, K)) != BL_OK) return st;
+  if (M > 0 && M >= kMaxElems / N) return BL_ERR_SHAPE;
+  return BL_OK;
+}
+
+template <int KIND>
+bl_status launch_grad(const bl::GradArgs& a, cudaStream_t stream) {
+  const int R = KIND == bl::kGradInput ? a.M : a.N;
+  const int rt = (R + 63) / 64;
+  bl::bl_grad_kernel<KIND><<<dim3(a.K / 64, rt < 65535 ? rt : 65535), 256, 0, stream>>>(a);
+  return last_cuda();
+}
+
+// Threads of a row kernel with c 16-byte chunks a thread.
+inline int row_threads(int K, int c) { return static_cast<int>(align_up((K / 8 + c - 1) / c, 32)); }
+
+// Chunks a thread holds of a row.
+inline int row_chunks(int K) { return K <= 2048 ? 1 : K <= 4096 ? 2 : K <= 8192 ? 4 : 8; }
+
+template <bool LAYER>
+bl_status launch_norm_fwd(const uint16_t* X, const uint16_t* w, const uint16_t* b, float eps, int m, int k,
+                          uint16_t* Y, float* mean, float* stat, cudaStream_t stream) {
+  const int c = row_chunks(k), t = row_threads(k, c);
+  switch (c) {
+    case 1: bl::bl_norm_fwd_kernel<1, LAYER><<<m, t, 0, stream>>>(X, w, b, eps, k, Y, mean, stat); break;
+    case 2: bl::bl_norm_fwd_kernel<2, LAYER><<<m, t, 0, stream>>>(X, w, b, eps, k, Y, mean, stat); break;
+    case 4: bl::bl_norm_fwd_kernel<4, LAYER><<<m, t, 0, stream>>>(X, w, b, eps, k, Y, mean, stat); break;
+    default: bl::bl_norm_fwd_kernel<8, LAYER><<<m, t, 0, stream>>>(X, w, b, eps, k, Y, mean, stat); break;
+  }
+  return last_cuda();
+}
+
+// Row gradients only.
+template <bool LAYER, bool CKPT>
+bl_status launch_norm_dx(const bl::NormGradArgs& a, cudaStream_t stream) {
+  const int c = row_chunks(a.K), t = row_threads(a.K, c);
+  switch (c) {
+    case 1: bl::bl_norm_bwd_kernel<1, LAYER, CKPT, false><<<a.M, t, 0, stream>>>(a); break;
+    case 2: bl::bl_norm_bwd_kernel<2, LAYER, CKPT, false><<<a.M, t, 0, stream>>>(a); break;
+    case 4: bl::bl_norm_bwd_kernel<4, LAYER, CKPT, false><<<a.M, t, 0, stream>>>(a); break;
+    default: bl::bl_norm_bwd_kernel<8, LAYER, CKPT, false><<<a.M, t, 0, stream>>>(a); break;
+  }
+  return last_cuda();
+}
+
+// Partial rows of dweight / dbias: one a CTA for rows that fit registers; for
+// wide rows enough row ranges to fill the GPU with the columns' CTAs.
+inline int norm_parts(int64_t M, int64_t K) {
+  if (K <= bl::kNgRowMaxK) return static_cast<int>(std::min<int64_t>(M, bl::kNgMaxParts));
+  const int64_t want = std::max<int64_t>(1, (int64_t(1184) * 1024) / K);
+  return static_cast<int>(std::min<int64_t>((M + 7) / 8, want));
+}
+
+template <bool LAYER>
+bl_status launch_norm_bwd(bl::NormGradArgs a, float* dweight, float* dbias, int accumulate, cudaStream_t stream) {
+  if (!dweight && !dbias) return launch_norm_dx<LAYER, false>(a, stream);
+  bl_status st;
+  int parts = norm_parts(a.M, a.K);
+  if (a.K <= bl::kNgRowMaxK) {
+    const int c = a.K <= 4096 ? 1 : 2, t = row_threads(a.K, c);
+    if (c == 1)
+      bl::bl_norm_bwd_kernel<1, LAYER, false, true><<<parts, t, 0, stream>>>(a);
+    else
+      bl::bl_norm_bwd_kernel<2, LAYER, false, true><<<parts, t, 0, stream>>>(a);
+    if ((st = last_cuda()) != BL_OK) return st;
+  } else {
+    // the columns first: dX may overwrite dY or X
+    const int per = (a.M + parts - 1) / parts;
+    parts = (a.M + per - 1) / per;
+    bl::bl_norm_wgrad_cols_kernel<LAYER><<<dim3((a.K / 8 + 127) / 128, parts), 128, 0, stream>>>(a, per);
+    if ((st = last_cuda()) != BL_OK) return st;
+    if (a.dX && (st = launch_norm_dx<LAYER, false>(a, stream)) != BL_OK) return st;
+  }
+  bl::bl_norm_wgrad_join_kernel<<<a.K / 16, 1024, 0, stream>>>(a.part, parts, a.K, dweight, dbias, accumulate);
+  return last_cuda();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bl_forward_checkpoint_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits) {
+  (void)bits;
+  if (check_shape_nk(N, K) != BL_OK || check_m(M, K) != BL_OK) return 0;
+  return align_up(static_cast<size_t>(M) * 4, 256);
+}
+
+bl_status bl_forward_checkpoint(const uint16_t* X, int norm, float eps, int64_t M, int64_t K, int64_t N,
+                                const uint8_t* Wp, const float* gamma, int bits, uint16_t* Y, int8_t* Xq,
+                                float* scale, float* stat, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  const NvtxRange nvtx_range("bl_forward_checkpoint");
+  bl_status st = check_shape_nk(N, K);
+  if (st != BL_OK) return st;
+  if ((st = check_m(M, K)) != BL_OK) return st;
+  if (bits != 8 && bits != 4) return BL_ERR_UNSUPPORTED;
+  if (norm != BL_NORM_NONE && norm != BL_NORM_RMS && norm != BL_NORM_LAYER) return BL_ERR_UNSUPPORTED;
+  if (norm != BL_NORM_NONE && !rms_eps_ok(eps)) return BL_ERR_INVALID_ARG;
+  if (M == 0) return BL_OK;
+  if (!X || !Wp || !gamma || !Y || !Xq || !scale || (norm != BL_NORM_NONE && !stat)) return BL_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Wp) || !aligned16(Xq) || !aligned4(scale) || !aligned4(stat))
+    return BL_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < bl_forward_checkpoint_workspace_bytes(M, K, N, bits)) return BL_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
+  const int Q = bits == 8 ? 127 : 7;
+  const int m = static_cast<int>(M), k = static_cast<int>(K);
+  int* R = static_cast<int*>(workspace);
+  if (norm == BL_NORM_NONE)
+    st = launch_act_quant(X, m, k, Q, Xq, scale, R, stream);
+  else if (norm == BL_NORM_LAYER)
+    st = launch_norm_quant(norm, X, nullptr, eps, m, k, Q, Xq, scale, R, nullptr, stat, stream);
+  else
+    st = launch_norm_quant(norm, X, nullptr, eps, m, k, Q, Xq, scale, R, stat, nullptr, stream);
+  if (st != BL_OK) return st;
+  return launch_tc(Xq, m, k, static_cast<int>(N), Wp, R, scale, gamma, Y, bl::kOutBF16, stream);
+}
+
+size_t bl_backward_input_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  (void)M;
+  (void)K;
+  (void)N;
+  return 0;
+}
+
+bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* Wp,
+                            const float* gamma, uint16_t* dX, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  const NvtxRange nvtx_range("bl_backward_input");
+  bl_status st = check_mnk(M, N, K);
+  if (st != BL_OK) return st;
+  if (M == 0) return BL_OK;
+  if (!dY || !Wp || !gamma || !dX) return BL_ERR_INVALID_ARG;
+  if (!aligned16(dY) || !aligned16(Wp) || !aligned16(dX) || !aligned4(gamma)) return BL_ERR_ALIGNMENT;
+  const size_t need = bl_backward_input_workspace_bytes(M, K, N);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return BL_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
+  }
+  bl::GradArgs a = {};
+  a.dY = dY;
+  a.A = Wp;
+  a.gamma = gamma;
+  a.out = dX;
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.out_bf16 = 1;
+  return launch_grad<bl::kGradInput>(a, stream);
+}
+
+size_t bl_backward_weight_workspace_bytes(int64_t M, int64_t K, int64_t N, unsigned flags) {
+  (void)M;
+  (void)K;
+  (void)N;
+  (void)flags;
+  return 0;
+}
+
+bl_status bl_backward_weight(const uint16_t* dY, const int8_t* Xq, const float* scale, int64_t M, int64_t K,
+                             int64_t N, unsigned flags, void* dW, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+  const NvtxRange nvtx_range("bl_backward_weight");
+  bl_status st = check_mnk(M, N, K);
+  if (st != BL_OK) return st;
+  if ((flags & ~(BL_GRAD_ACCUMULATE | BL_GRAD_BF16)) != 0u) return BL_ERR_UNSUPPORTED;
+  if (!dW) return BL_ERR_INVALID_ARG;
+  if (!aligned16(dW)) return BL_ERR_ALIGNMENT;
+  if (M == 0) {   // an empty sum
+    if (flags & BL_GRAD_ACCUMULATE) return BL_OK;
+    const size_t bytes = static_cast<size_t>(N) * static_cast<size_t>(K) * ((flags & BL_GRAD_BF16) ? 2 : 4);
+    return cudaMemsetAsync(dW, 0, bytes, stream) == cudaSuccess ? BL_OK : BL_ERR_CUDA;
+  }
+  if (!dY || !Xq || !scale) return BL_ERR_INVALID_ARG;
+  if (!aligned16(dY) || !aligned16(Xq) || !aligned4(scale)) return BL_ERR_ALIGNMENT;
+  const size_t need = bl_backward_weight_workspace_bytes(M, K, N, flags);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return BL_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
+  }
+  bl::GradArgs a = {};
+  a.dY = dY;
+  a.A = reinterpret_cast<const uint8_t*>(Xq);
+  a.scale = scale;
+  a.out = dW;
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.out_bf16 = (flags & BL_GRAD_BF16) ? 1 : 0;
+  a.accumulate = (flags & BL_GRAD_ACCUMULATE) ? 1 : 0;
+  return launch_grad<bl::kGradWeight>(a, stream);
+}
+
+bl_status bl_norm_forward(const uint16_t* X, const uint16_t* weight, const uint16_t* bias, int norm, float eps,
+                          int64_t M, int64_t K, uint16_t* Y, float* mean, float* stat, cudaStream_t stream) {
+  const NvtxRange nvtx_range("bl_norm_forward");
+  bl_status st = check_rows(M, K);
+  if (st != BL_OK) return st;
+  if (norm != BL_NORM_RMS && norm != BL_NORM_LAYER) return BL_ERR_UNSUPPORTED;
+  if (!rms_eps_ok(eps) || (norm == BL_NORM_RMS && mean)) return BL_ERR_INVALID_ARG;
+  if (M == 0) return BL_OK;
+  if (!X || !Y) return BL_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(weight) || !aligned16(bias) || !aligned4(mean) || !aligned4(stat))
+    return BL_ERR_ALIGNMENT;
+  const int m = static_cast<int>(M), k = static_cast<int>(K);
+  if (norm == BL_NORM_LAYER) return launch_norm_fwd<true>(X, weight, bias, eps, m, k, Y, mean, stat, stream);
+  return launch_norm_fwd<false>(X, weight, bias, eps, m, k, Y, nullptr, stat, stream);
+}
+
+size_t bl_norm_backward_workspace_bytes(int64_t M, int64_t K) {
+  if (check_rows(M, K) != BL_OK || M == 0) return 0;
+  return static_cast<size_t>(norm_parts(M, K)) * 2 * static_cast<size_t>(K) * sizeof(float);
+}
+
+bl_status bl_norm_backward(const uint16_t* dY, const uint16_t* X, const uint16_t* weight, int norm, float eps,
+                           const float* mean, const float* stat, int64_t M, int64_t K, unsigned flags, uint16_t* dX,
+                           float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  const NvtxRange nvtx_range("bl_norm_backward");
+  bl_status st = check_rows(M, K);
+  if (st != BL_OK) return st;
+  if (norm != BL_NORM_RMS && norm != BL_NORM_LAYER) return BL_ERR_UNSUPPORTED;
+  if ((flags & ~BL_GRAD_ACCUMULATE) != 0u) return BL_ERR_UNSUPPORTED;
+  if (!rms_eps_ok(eps) || (norm == BL_NORM_RMS && mean) || (!dX && !dweight && !dbias)) return BL_ERR_INVALID_ARG;
+  if (!aligned16(dweight) || !aligned16(dbias)) return BL_ERR_ALIGNMENT;
+  const int accumulate = (flags & BL_GRAD_ACCUMULATE) ? 1 : 0;
+  if (M == 0) {   // empty sums
+    const size_t bytes = static_cast<size_t>(K) * sizeof(float);
+    if (!accumulate && dweight && cudaMemsetAsync(dweight, 0, bytes, stream) != cudaSuccess) return BL_ERR_CUDA;
+    if (!accumulate && dbias && cudaMemsetAsync(dbias, 0, bytes, stream) != cudaSuccess) return BL_ERR_CUDA;
+    return BL_OK;
+  }
+  if (!dY || !X || !stat || (norm == BL_NORM_LAYER && !mean)) return BL_ERR_INVALID_ARG;
+  if (!aligned16(dY) || !aligned16(X) || !aligned16(weight) || !aligned16(dX) || !aligned4(mean) || !aligned4(stat))
+    return BL_ERR_ALIGNMENT;
+  if (dweight || dbias) {
+    if (!workspace || workspace_bytes < bl_norm_backward_workspace_bytes(M, K)) return BL_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
+  }
+  bl::NormGradArgs a = {};
+  a.dY = dY;
+  a.X = X;
+  a.weight = weight;
+  a.mean = mean;
+  a.stat = stat;
+  a.dX = dX;
+  a.part = static_cast<float*>(workspace);
+  a.eps = eps;
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  if (norm == BL_NORM_LAYER) return launch_norm_bwd<true>(a, dweight, dbias, accumulate, stream);
+  return launch_norm_bwd<false>(a, dweight, dbias, accumulate, stream);
+}
+
+bl_status bl_norm_backward_checkpoint(const uint16_t* dXn, const int8_t* Xq, const float* scale, int norm, float eps,
+                                      const float* stat, int64_t M, int64_t K, uint16_t* dX, cudaStream_t stream) {
+  const NvtxRange nvtx_range("bl_norm_backward_checkpoint");
+  bl_status st = check_rows(M, K);
+  if (st != BL_OK) return st;
+  if (norm != BL_NORM_RMS && norm != BL_NORM_LAYER) return BL_ERR_UNSUPPORTED;
+  if (!rms_eps_ok(eps)) return BL_ERR_INVALID_ARG;
+  if (M == 0) return BL_OK;
+  if (!dXn || !Xq || !scale || !stat || !dX) return BL_ERR_INVALID_ARG;
+  if (!aligned16(dXn) || !aligned16(Xq) || !aligned16(dX) || !aligned4(scale) || !aligned4(stat))
+    return BL_ERR_ALIGNMENT;
+  bl::NormGradArgs a = {};
+  a.dY = dXn;
+  a.Xq = Xq;
+  a.scale = scale;
+  a.stat = stat;
+  a.dX = dX;
+  a.eps = eps;
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  if (norm == BL_NORM_LAYER) return launch_norm_dx<true, true>(a, stream);
+  return launch_norm_dx<false, true>(a, stream);
+}
+
 // ---------------------------------------------------------------------------
 // Base-3 weight storage (five weights a byte; see bl_weights.cuh).
 // ---------------------------------------------------------------------------
-
 size_t bl_packed_weight_bytes_b3(int64_t N, int64_t K) {
   if (check_shape_nk(N, K) != BL_OK) return 0;
   return static_cast<size_t>(N) * 4u * static_cast<size_t>(bl::base3_row_words(static_cast<int>(K)));

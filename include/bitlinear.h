@@ -413,6 +413,120 @@ BL_API bl_status bl_forward_norm_grouped(int count, const bl_linear* problems, i
                                          const uint16_t* const* norm_weights, float eps, int bits, void* workspace,
                                          size_t workspace_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Training: a forward that keeps its activations as 8-bit codes, the gradients
+ * that go back through it, and a norm with its own backward.  The pages train
+ * with the straight-through estimator: round and clamp have derivative one,
+ * and the scales gamma and s_m are constants.  With the forward
+ *   Y = (q / s) (gamma C)^T,  C the ternary codes [N, K],
+ * the gradients for dY = dLoss/dY (bf16 [M, N]) are
+ *   dX = gamma * dY C              dW = dY^T (q / s)
+ * (dW is the gradient of the latent weights W).  What has to be kept between
+ * the two passes is M*K bytes of codes and 4*M bytes of scales, half of the
+ * bf16 activations, and it is exactly what the forward multiplied.
+ * Values of dY that are NaN or Inf give undefined (but memory-safe) results.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * bl_forward (norm == BL_NORM_NONE), bl_forward_rmsnorm without a weight
+ * (BL_NORM_RMS) or bl_forward_layernorm (BL_NORM_LAYER), bit for bit, that
+ * leaves the activation checkpoint with the caller:
+ *   Xq int8 [M, K] (16-byte aligned), scale fp32 [M]   as bl_quant_act
+ *   stat fp32 [M]   the mean of squares (RMS) or the biased variance (LAYER)
+ *                   of every token; not written, and may be NULL, without a norm
+ * bits = 4 codes are stored one a byte.  eps is ignored without a norm.
+ * workspace: bl_forward_checkpoint_workspace_bytes(M, K, N, bits) bytes,
+ * 16-byte aligned.  The ordering rule of bl_forward applies.
+ */
+#define BL_NORM_NONE 2
+BL_API size_t bl_forward_checkpoint_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits);
+BL_API bl_status bl_forward_checkpoint(const uint16_t* X, int norm, float eps, int64_t M, int64_t K, int64_t N,
+                                       const uint8_t* Wp, const float* gamma, int bits, uint16_t* Y, int8_t* Xq,
+                                       float* scale, float* stat, void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream);
+
+/*
+ * Gradient of the (normalised) input:
+ *   dX[m,k] = bf16_rn( gamma * sum_n dY[m,n] * C[n,k] )     fp32 sums
+ * dY: bf16 bits [M, N], 16-byte aligned.  Wp, gamma as in bl_forward.  dX:
+ * bf16 bits [M, K], 16-byte aligned.  Any N; M == 0 is a no-op.  Results do
+ * not depend on the run (no atomics).  workspace:
+ * bl_backward_input_workspace_bytes(M, K, N) bytes (may be 0), 16-byte aligned.
+ */
+BL_API size_t bl_backward_input_workspace_bytes(int64_t M, int64_t K, int64_t N);
+BL_API bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* Wp,
+                                   const float* gamma, uint16_t* dX, void* workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
+
+/*
+ * Gradient of the latent weights from the activation checkpoint:
+ *   dW[n,k] = sum_m dY[m,n] * Xq[m,k] / scale[m]            fp32 sums
+ * flags: 0, or an OR of
+ *   BL_GRAD_ACCUMULATE  dW += instead of dW = (gradient accumulation over
+ *                       micro-batches)
+ *   BL_GRAD_BF16        dW is bf16 [N, K] instead of fp32
+ * An fp32 dW takes Xq / scale as the sum of two bf16 (relative error 2^-16 a
+ * product at most), a bf16 dW as one bf16 (2^-8, like its own rounding): half
+ * the tensor-core work.
+ * dY: bf16 bits [M, N], 16-byte aligned.  Xq: int8 [M, K], 16-byte aligned.
+ * scale: fp32 [M], positive, 4-byte aligned.  dW: 16-byte aligned.  Any N.
+ * M == 0 writes zeros (nothing with BL_GRAD_ACCUMULATE).  Results do not
+ * depend on the run.  workspace: bl_backward_weight_workspace_bytes(M, K, N,
+ * flags) bytes (may be 0), 16-byte aligned.
+ */
+#define BL_GRAD_ACCUMULATE 1u
+#define BL_GRAD_BF16 2u
+BL_API size_t bl_backward_weight_workspace_bytes(int64_t M, int64_t K, int64_t N, unsigned flags);
+BL_API bl_status bl_backward_weight(const uint16_t* dY, const int8_t* Xq, const float* scale, int64_t M, int64_t K,
+                                    int64_t N, unsigned flags, void* dW, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/*
+ * RMSNorm (norm == BL_NORM_RMS) or LayerNorm (BL_NORM_LAYER) of bf16 rows as
+ * an operator of its own (e.g. before the output head), in fp32:
+ *   LAYER: mu = (1/K) sum_k x, stat = (1/K) sum_k (x - mu)^2
+ *   RMS:   mu = 0,             stat = (1/K) sum_k x^2
+ *   Y = bf16_rn( (x - mu) / sqrt(stat + eps) * weight + bias )
+ * X, Y: bf16 bits [M, K], 16-byte aligned; Y may be X.  weight, bias: bf16
+ * bits [K], 16-byte aligned, or NULL.  mean: fp32 [M] (LAYER; may be NULL,
+ * must be NULL for RMS), stat: fp32 [M] or NULL: what bl_norm_backward needs.
+ * Unlike the normalising forwards above, the statistics are plain fp32 sums.
+ * eps positive and finite.  K % 64 == 0.  M == 0 is a no-op.
+ */
+BL_API bl_status bl_norm_forward(const uint16_t* X, const uint16_t* weight, const uint16_t* bias, int norm, float eps,
+                                 int64_t M, int64_t K, uint16_t* Y, float* mean, float* stat, cudaStream_t stream);
+
+/*
+ * Its gradients, in fp32, with xh = (x - mean) / sqrt(stat + eps), g = dY * weight:
+ *   dX      = bf16_rn( (g - xh * mean_k(g xh) [- mean_k(g), LAYER]) / sqrt(stat + eps) )
+ *   dweight = sum_m dY xh     dbias = sum_m dY          fp32 [K]
+ * dY, X, dX: bf16 bits [M, K], 16-byte aligned; dX may be dY or X.  weight or NULL.
+ * mean (NULL for RMS), stat: fp32 [M] as written by the forward.  dX, dweight
+ * and dbias may each be NULL (not wanted; all three is an error); dweight,
+ * dbias 16-byte aligned.  flags: 0 or BL_GRAD_ACCUMULATE (dweight += ...,
+ * dbias += ...).  M == 0 writes zeros to dweight and dbias (nothing with
+ * BL_GRAD_ACCUMULATE).  Results do not depend on the run.
+ * workspace: bl_norm_backward_workspace_bytes(M, K) bytes, 16-byte aligned
+ * (may be null when neither dweight nor dbias is wanted).
+ */
+BL_API size_t bl_norm_backward_workspace_bytes(int64_t M, int64_t K);
+BL_API bl_status bl_norm_backward(const uint16_t* dY, const uint16_t* X, const uint16_t* weight, int norm, float eps,
+                                  const float* mean, const float* stat, int64_t M, int64_t K, unsigned flags,
+                                  uint16_t* dX, float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/*
+ * The backward of the norm inside bl_forward_checkpoint, from the checkpoint
+ * alone (the norm's bf16 input is not kept): the normalised value is read back
+ * as xh = Xq / scale, straight through the quantiser,
+ *   dX = bf16_rn( (dXn - xh * mean_k(dXn xh) [- mean_k(dXn), LAYER]) / sqrt(stat + eps) )
+ * with dXn: bf16 bits [M, K] from bl_backward_input, 16-byte aligned; dX may
+ * be dXn.  Xq, scale, stat, norm and eps as in bl_forward_checkpoint.
+ */
+BL_API bl_status bl_norm_backward_checkpoint(const uint16_t* dXn, const int8_t* Xq, const float* scale, int norm,
+                                             float eps, const float* stat, int64_t M, int64_t K, uint16_t* dX,
+                                             cudaStream_t stream);
+
 /* Device workspace bytes bl_matmul_i32 needs (0 when M <= 2). */
 BL_API size_t bl_matmul_i32_workspace_bytes(int64_t M, int64_t K, int64_t N);
 
