@@ -26,6 +26,7 @@
 #include "bl_gemv.cuh"
 #include "bl_grad.cuh"
 #include "bl_norm_grad.cuh"
+#include "bl_grad_tc.cuh"
 #include "bl_decode.cuh"
 #include "bl_probe.cuh"
 #include "bl_weights.cuh"
@@ -1605,11 +1606,143 @@ bl_status check_mnk(int64_t M, int64_t N, int64_t K) {
   return BL_OK;
 }
 
+// How a gradient is cut into tiles and parts of its sum: from the shape alone,
+// so that the workspace queries need no device.
+struct GradPlan {
+  int bn;                // r of a tile
+  int kt, rt;            // tiles along k and r
+  int splits, per;       // parts of the sum, stages a part
+  int64_t ld;            // row stride of dY in elements (N, or a padded copy's)
+  size_t pad_bytes, part_bytes;
+};
+
+constexpr int kGradPlanPairs = 74;   // CTA pairs of a B200
+
+GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N) {
+  GradPlan g = {};
+  const int64_t R = kind == bl::kGradInput ? M : N, L = kind == bl::kGradInput ? N : M;
+  g.bn = R > 128 ? 256 : R > 64 || kind == bl::kGradWeight ? 128 : R > 32 ? 64 : 32;
+  const int64_t kt = (K + 2 * bl::kGtK - 1) / (2 * bl::kGtK), rt = (R + g.bn - 1) / g.bn;
+  const int64_t nk = (L + bl::kGtBC - 1) / bl::kGtBC, tiles = kt * rt;
+  g.kt = static_cast<int>(kt);
+  g.rt = static_cast<int>(rt);
+  int64_t splits = 1;
+  if (2 * tiles <= kGradPlanPairs) splits = std::max<int64_t>(1, std::min<int64_t>(kGradPlanPairs / tiles, nk / 4));
+  g.per = static_cast<int>((nk + splits - 1) / splits);
+  g.splits = static_cast<int>((nk + g.per - 1) / g.per);
+  g.ld = static_cast<int64_t>(align_up(static_cast<size_t>(N), 8));
+  g.pad_bytes = g.ld == N ? 0 : align_up(static_cast<size_t>(M) * g.ld * 2, 256);
+  g.part_bytes = g.splits > 1 ? static_cast<size_t>(g.splits) * R * K * sizeof(float) : 0;
+  return g;
+}
+
+// 2-D tensor map [rows, cols] with a row stride in bytes.
+bool encode_2d(CUtensorMap* tm, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t cols,
+               uint64_t stride, uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swz) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {stride};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(tm, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KIND, int TERMS, int BN>
+bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t* dY, float* parts,
+                        cudaStream_t stream) {
+  using C = bl::GtCfg<KIND, TERMS, BN>;
+  auto kern = bl::bl_grad_pair_kernel<KIND, TERMS, BN>;
+  static std::atomic<uint64_t> done{0};
+  if (!ensure_smem(kern, C::kSmemBytes, &done)) return BL_ERR_CUDA;
+  const uint64_t M = a.M, K = a.K, N = a.N;
+  CUtensorMap tmA, tmB, tmD;
+  bl::GtArgs P = {};
+  P.scale = a.scale;
+  P.gamma = g.splits > 1 ? nullptr : a.gamma;
+  P.R = KIND == bl::kGradInput ? a.M : a.N;
+  P.L = KIND == bl::kGradInput ? a.N : a.M;
+  P.K = a.K;
+  P.kt = g.kt;
+  P.rt = g.rt;
+  P.splits = g.splits;
+  P.per = g.per;
+  if (g.splits > 1) {
+    P.out = parts;
+    P.mode = bl::kGtF32;
+  } else {
+    P.out = a.out;
+    P.mode = !a.out_bf16 ? (a.accumulate ? bl::kGtF32Acc : bl::kGtF32) : (a.accumulate ? bl::kGtBf16Acc : bl::kGtTmaBf16);
+  }
+  const bool ok =
+      (KIND == bl::kGradInput ? encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, N, K / 4, K / 4, bl::kGtBC,
+                                          bl::kGtK / 4, CU_TENSOR_MAP_SWIZZLE_NONE)
+                              : encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, M, K, K, bl::kGtBC, bl::kGtK,
+                                          CU_TENSOR_MAP_SWIZZLE_NONE)) &&
+      encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, M, N, static_cast<uint64_t>(g.ld) * 2,
+                KIND == bl::kGradInput ? C::kHalf : bl::kGtBC, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!ok) return BL_ERR_CUDA;
+  if (P.mode == bl::kGtTmaBf16) {
+    if (!encode_2d(&tmD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, static_cast<uint64_t>(P.R), K, K * 2, C::kChunk, 32,
+                   CU_TENSOR_MAP_SWIZZLE_NONE))
+      return BL_ERR_CUDA;
+  } else {
+    tmD = tmB;   // not used
+  }
+  int npairs = max_active_pairs(kern, C::kThreads, C::kSmemBytes);
+  if (npairs <= 0) return BL_ERR_CUDA;
+  const int64_t items = static_cast<int64_t>(g.kt) * g.rt * g.splits;
+  if (npairs > items) npairs = static_cast<int>(items);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * npairs);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const unsigned long long lim = kWaitLimitNs;
+  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, P, lim) != cudaSuccess) return BL_ERR_CUDA;
+  return last_cuda();
+}
+
 template <int KIND>
-bl_status launch_grad(const bl::GradArgs& a, cudaStream_t stream) {
-  const int R = KIND == bl::kGradInput ? a.M : a.N;
-  const int rt = (R + 63) / 64;
-  bl::bl_grad_kernel<KIND><<<dim3(a.K / 64, rt < 65535 ? rt : 65535), 256, 0, stream>>>(a);
+bl_status launch_grad(const bl::GradArgs& a, void* workspace, cudaStream_t stream) {
+  const GradPlan g = plan_grad(KIND, a.M, a.K, a.N);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const uint16_t* dY = a.dY;
+  bl_status st;
+  if (g.pad_bytes) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(ws);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((g.ld + 255) / 256, 64)), std::min(a.M, 16384));
+    bl::bl_grad_pad_kernel<<<grid, 256, 0, stream>>>(a.dY, p, a.M, a.N, static_cast<int>(g.ld));
+    if ((st = last_cuda()) != BL_OK) return st;
+    dY = p;
+  }
+  float* parts = reinterpret_cast<float*>(ws + g.pad_bytes);
+  if constexpr (KIND == bl::kGradInput) {
+    switch (g.bn) {
+      case 32: st = launch_grad_t<KIND, 1, 32>(a, g, dY, parts, stream); break;
+      case 64: st = launch_grad_t<KIND, 1, 64>(a, g, dY, parts, stream); break;
+      case 128: st = launch_grad_t<KIND, 1, 128>(a, g, dY, parts, stream); break;
+      default: st = launch_grad_t<KIND, 1, 256>(a, g, dY, parts, stream); break;
+    }
+  } else if (a.out_bf16) {
+    st = g.bn == 128 ? launch_grad_t<KIND, 1, 128>(a, g, dY, parts, stream)
+                     : launch_grad_t<KIND, 1, 256>(a, g, dY, parts, stream);
+  } else {
+    st = g.bn == 128 ? launch_grad_t<KIND, 2, 128>(a, g, dY, parts, stream)
+                     : launch_grad_t<KIND, 2, 256>(a, g, dY, parts, stream);
+  }
+  if (st != BL_OK || g.splits == 1) return st;
+  const size_t n4 = static_cast<size_t>(KIND == bl::kGradInput ? a.M : a.N) * a.K / 4;
+  bl::bl_grad_join_kernel<<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, stream>>>(
+      parts, g.splits, n4, a.gamma, a.out, a.out_bf16, a.accumulate);
   return last_cuda();
 }
 
@@ -1718,10 +1851,9 @@ bl_status bl_forward_checkpoint(const uint16_t* X, int norm, float eps, int64_t 
 }
 
 size_t bl_backward_input_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  (void)M;
-  (void)K;
-  (void)N;
-  return 0;
+  if (check_mnk(M, N, K) != BL_OK || M == 0) return 0;
+  const GradPlan g = plan_grad(bl::kGradInput, M, K, N);
+  return g.pad_bytes + g.part_bytes;
 }
 
 bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* Wp,
@@ -1747,15 +1879,14 @@ bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
   a.K = static_cast<int>(K);
   a.N = static_cast<int>(N);
   a.out_bf16 = 1;
-  return launch_grad<bl::kGradInput>(a, stream);
+  return launch_grad<bl::kGradInput>(a, workspace, stream);
 }
 
 size_t bl_backward_weight_workspace_bytes(int64_t M, int64_t K, int64_t N, unsigned flags) {
-  (void)M;
-  (void)K;
-  (void)N;
   (void)flags;
-  return 0;
+  if (check_mnk(M, N, K) != BL_OK || M == 0) return 0;
+  const GradPlan g = plan_grad(bl::kGradWeight, M, K, N);
+  return g.pad_bytes + g.part_bytes;
 }
 
 bl_status bl_backward_weight(const uint16_t* dY, const int8_t* Xq, const float* scale, int64_t M, int64_t K,
@@ -1789,7 +1920,7 @@ bl_status bl_backward_weight(const uint16_t* dY, const int8_t* Xq, const float* 
   a.N = static_cast<int>(N);
   a.out_bf16 = (flags & BL_GRAD_BF16) ? 1 : 0;
   a.accumulate = (flags & BL_GRAD_ACCUMULATE) ? 1 : 0;
-  return launch_grad<bl::kGradWeight>(a, stream);
+  return launch_grad<bl::kGradWeight>(a, workspace, stream);
 }
 
 bl_status bl_norm_forward(const uint16_t* X, const uint16_t* weight, const uint16_t* bias, int norm, float eps,

@@ -1,0 +1,541 @@
+// Gradients through the ternary matmul on the tensor cores (tcgen05 kind::f16,
+// CTA pairs, bf16 operands, fp32 accumulators in tensor memory).
+//
+// Straight-through gradients of Y = (q / s) (gamma C)^T ("BitNet b1.58: The
+// 1-Bit Ternary LLM Architecture Guide", section "The Mathematical Formulation
+// of BitLinear", eq. (3)):
+//   input   dX[m, k] = gamma sum_n dY[m, n] C[n, k]
+//   weight  dW[n, k] = sum_m dY[m, n] q[m, k] / s[m]
+// Both are D[k, r] = sum_c A[c, k] B[r, c]: A the stored low-bit matrix with
+// k contiguous (packed ternary rows c = n, or int8 codes with rows c = m and a
+// scale a row), B a view of dY (r = m, c contiguous; or r = n, r contiguous).
+//
+// A pair of CTAs computes 256 (k) x BN (r) per tile:
+//   * every CTA brings its 128 k of the raw low-bit rows and half of the tile
+//     of dY into shared memory with TMA, 64 rows of the sum a stage;
+//   * converter warps expand the raw rows to bf16 into the swizzled operand
+//     tile next to them (k contiguous: an MN-major operand, so nothing is
+//     transposed).  C is exact in bf16.  q / s is not: an fp32 result takes it
+//     as hi + lo, two bf16 with 2^-16 relative error together, and twice the
+//     MMAs; a bf16 result takes hi alone, off by half a step of its own type;
+//   * the leader issues tcgen05.mma.cta_group::2 (M = 256, N = BN, K = 16),
+//     each tensor core reading only its half of dY from its own SM;
+//   * eight epilogue warps drain one accumulator while the next one fills.
+//     Lanes are k, so a warp's store of one r is 32 neighbouring k.
+// The low-bit matrix is expanded once per tile and never exists in memory as
+// bf16; A's conversion runs beside the MMAs.
+// Few tiles, long sum: the sum is split over pairs; the parts (fp32) meet in
+// bl_grad_join_kernel in a fixed order.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "bl_common.cuh"
+#include "bl_grad.cuh"
+#include "bl_tc_common.cuh"
+
+namespace bl {
+
+constexpr int kGtBC = 64;                 // rows of the sum a stage
+constexpr int kGtK = 128;                 // k a CTA (256 a pair)
+constexpr int kGtABytes = kGtBC * kGtK * 2;   // one expanded operand tile: two 64-k blocks of 64 rows x 128 bytes
+constexpr int kGtEpiWarps = 8;
+
+// TERMS: bf16 terms of A (2: hi + lo).
+template <int KIND, int TERMS, int BN>
+struct GtCfg {
+  static constexpr int kHalf = BN / 2;                         // r rows staged per CTA
+  static constexpr int kBBytes = kHalf * kGtBC * 2;
+  static constexpr int kRawBytes = KIND == kGradInput ? kGtBC * kGtK / 4 : kGtBC * kGtK;
+  static constexpr int kStageBytes = TERMS * kGtABytes + kBBytes + kRawBytes;
+  static constexpr int kConvWarps = KIND == kGradInput ? 4 : 8;
+  static constexpr int kFirstEpi = 2 + kConvWarps;
+  static constexpr int kThreads = 32 * (kFirstEpi + kGtEpiWarps);
+  static constexpr int kChunk = kHalf < 32 ? kHalf : 32;       // r of one epilogue step
+  static constexpr int kOutBytes = 2 * kChunk * 64;            // two bf16 staging tiles [r][32 k] a warp
+  static constexpr int kOutTotal = kGtEpiWarps * kOutBytes;
+  static constexpr int kBudget = 227 * 1024 - 1024 - 512 - kOutTotal;
+  static constexpr int kMaxStages = kBudget / kStageBytes;
+  static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
+  static constexpr int kOutOffset = kStages * kStageBytes;
+  static constexpr int kBarOffset = kOutOffset + kOutTotal;
+  static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
+  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+  static_assert(kStages >= 2 && kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(kStageBytes % 1024 == 0, "stage tiles are 1024-byte aligned");
+  static_assert((3 * kStages + 5) * 8 + 8 <= 512, "barriers");
+};
+
+struct GtArgs {
+  const float* scale;   // [M] (weight)
+  const float* gamma;   // device scalar (input), else null
+  void* out;            // final output, or fp32 parts [splits][R][K]
+  int R, L, K;          // output rows, length of the sum, columns
+  int kt, rt;           // tiles along k and r
+  int splits, per;      // parts of the sum, stages a part
+  int mode;             // GtOut
+};
+enum GtOut : int { kGtTmaBf16 = 0, kGtF32 = 1, kGtF32Acc = 2, kGtBf16Acc = 3 };
+
+// Instruction descriptor: kind::f16, bf16 x bf16 -> f32; A MN-major, B
+// MN-major or K-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool b_mn) {
+  return (1u << 4)                                   // D: f32
+         | (1u << 7) | (1u << 10)                    // A, B: bf16
+         | (1u << 15)                                // A: MN-major
+         | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// High words of the operand descriptors (128-byte swizzle, 8-row atoms 1024
+// bytes apart); the low word is the start address and, for MN-major operands,
+// the 8192 bytes between blocks of 64 elements.
+constexpr uint32_t kGtDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t gt_desc_mn_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | ((8192u >> 4) << 16); }
+__device__ __forceinline__ uint32_t gt_desc_k_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
+
+__device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(kGtDescHi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on CTA 0's copy of a barrier after generic shared-memory writes that
+// the tensor cores read: every writer has passed fence.proxy.async and the
+// warp has met.
+__device__ __forceinline__ void gt_arrive_leader(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
+      "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// Sixteen packed codes -> sixteen bf16 in {-1, 0, 1}.  Slice j of the word has
+// the codes u = c + 1 of k = 4j..4j+3 in its bytes; u * 17 + 0x40 is the byte
+// with nibbles (u + 4, u), which pick the high and the low byte of bf16(u - 1)
+// from a table of six bytes.
+__device__ __forceinline__ void expand16(uint32_t w, uint32_t (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t sel = ((w >> (2 * j)) & 0x03030303u) * 17u + 0x40404040u;
+    v[2 * j] = __byte_perm(0x00800080u, 0x003F00BFu, sel);
+    v[2 * j + 1] = __byte_perm(0x00800080u, 0x003F00BFu, sel >> 16);
+  }
+}
+
+// Two codes (bytes B0, B0 + 1 of x, each q + 128) times r: the pair as fp32.
+// 0x4B0000xx is 2^23 + xx; the subtraction leaves q exactly.
+template <int B0>
+__device__ __forceinline__ uint64_t codes2_f32(uint32_t x, uint64_t rr) {
+  const uint32_t a = __byte_perm(x, 0x4B000000u, 0x7440 + B0), b = __byte_perm(x, 0x4B000000u, 0x7440 + B0 + 1);
+  uint64_t v;
+  asm("{\n\t.reg .b64 t, o;\n\t"
+      "mov.b64 t, {%1, %2};\n\t"
+      "mov.b64 o, {%3, %3};\n\t"
+      "add.rn.f32x2 t, t, o;\n\t"
+      "mul.rn.f32x2 %0, t, %4;\n\t}"
+      : "=l"(v)
+      : "r"(a), "r"(b), "r"(0xCB000080u), "l"(rr));   // -(2^23 + 128)
+  return v;
+}
+
+// hi = bf16x2(v); lo = bf16x2(v - hi).
+template <int TERMS>
+__device__ __forceinline__ void split2(uint64_t v, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b32 a, b;\n\t"
+      "mov.b64 {a, b}, %1;\n\t"
+      "cvt.rn.bf16x2.f32 %0, b, a;\n\t}"
+      : "=r"(hi)
+      : "l"(v));
+  if (TERMS == 2) {
+    asm("{\n\t.reg .b32 a, b;\n\t.reg .b64 t;\n\t"
+        "shl.b32 a, %1, 16;\n\t"
+        "and.b32 b, %1, 0xffff0000;\n\t"
+        "mov.b64 t, {a, b};\n\t"
+        "sub.rn.f32x2 t, %2, t;\n\t"
+        "mov.b64 {a, b}, t;\n\t"
+        "cvt.rn.bf16x2.f32 %0, b, a;\n\t}"
+        : "=r"(lo)
+        : "r"(hi), "l"(v));
+  }
+}
+
+template <int KIND, int TERMS, int BN>
+__global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
+    bl_grad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmD, const GtArgs P, unsigned long long limit_ns) {
+  using C = GtCfg<KIND, TERMS, BN>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sOut = smem + C::kOutOffset;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);   // raw rows and dY have landed
+  uint64_t* done = full + S;                                           // the MMAs have read the stage
+  uint64_t* ready = done + S;       // leader's copy: both CTAs' converter warps have expanded the stage
+  uint64_t* accfull = ready + S;
+  uint64_t* accempty = accfull + 2;   // leader's copy: both CTAs' epilogue warps
+  uint64_t* drain = accempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int nk = (P.L + kGtBC - 1) / kGtBC;
+  const int nitems = P.kt * P.rt * P.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&done[s], 1);
+      mbar_init(&ready[s], 2 * C::kConvWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], 2 * kGtEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, C::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();   // barriers of both CTAs initialised before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // an item: tile (k fastest, so neighbouring pairs share a slab of dY) and part of the sum
+  auto item = [&](int it, int& kt, int& rt, int& c0, int& c1, int& part) {
+    const int tile = it % (P.kt * P.rt);
+    part = it / (P.kt * P.rt);
+    kt = tile % P.kt;
+    rt = tile / P.kt;
+    c0 = part * P.per;
+    c1 = min(nk, c0 + P.per);
+  };
+
+  if (warp == 0) {
+    // ---------------- TMA producer (both CTAs) ----------------
+    if (lane == 0) {
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmB);
+      uint32_t g = 0;
+      bool stop = false;
+      for (int it = pair; it < nitems && !stop; it += npairs) {
+        int kt, rt, c0, c1, part;
+        item(it, kt, rt, c0, c1, part);
+        const int k0 = kt * 2 * kGtK + static_cast<int>(rank) * kGtK;
+        const int r0 = rt * BN + static_cast<int>(rank) * C::kHalf;
+        for (int c = c0; c < c1; ++c, ++g) {
+          const int s = g % S;
+          if (g >= static_cast<uint32_t>(S) &&
+              !mbar_wait_cluster(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty)) {
+            stop = true;
+            break;
+          }
+          uint8_t* st = smem + s * C::kStageBytes;
+          uint8_t* sB = st + TERMS * kGtABytes;
+          mbar_arrive_expect_tx(&full[s], C::kBBytes + C::kRawBytes);
+          tma_load_2d(sB + C::kBBytes, &tmA, KIND == kGradInput ? k0 / 4 : k0, c * kGtBC, &full[s]);
+          if (KIND == kGradInput) {
+            tma_load_2d(sB, &tmB, c * kGtBC, r0, &full[s]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < C::kHalf / 64; ++j)
+              tma_load_2d(sB + j * 8192, &tmB, r0 + 64 * j, c * kGtBC, &full[s]);
+          }
+        }
+      }
+      const uint32_t issued = g;
+      for (uint32_t s = 0; s < static_cast<uint32_t>(S) && s < issued; ++s) {
+        const uint32_t last = s + S * ((issued - 1 - s) / S);
+        mbar_wait(&full[s], (last / S) & 1, nullptr, limit_ns, kSiteDrain);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (leader only) ----------------
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16(2 * kGtK, BN, KIND == kGradWeight);
+      const uint32_t base = smem_u32(smem);
+      int s = 0, i = 0;
+      uint32_t ph = 0;
+      bool stop = false;
+      for (int it = pair; it < nitems && !stop; it += npairs, ++i) {
+        int kt, rt, c0, c1, part;
+        item(it, kt, rt, c0, c1, part);
+        const int b = i & 1;
+        if (i >= 2 && !mbar_wait_cluster(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + b * BN;
+        for (int c = c0; c < c1; ++c) {
+          if (!mbar_wait_cluster(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = base + s * C::kStageBytes, sb = st + TERMS * kGtABytes;
+          const uint32_t blo = KIND == kGradInput ? gt_desc_k_lo(sb) : gt_desc_mn_lo(sb);
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t) {
+            const uint32_t alo = gt_desc_mn_lo(st + t * kGtABytes);
+#pragma unroll
+            for (int k = 0; k < kGtBC / 16; ++k)   // 16 rows of the sum: 2048 bytes MN-major, 32 bytes K-major
+              mma_bf16_ss_pair(d_tmem, alo + k * 128, blo + k * (KIND == kGradInput ? 2 : 128), idesc,
+                               (c != c0 || t != 0 || k != 0) ? 1u : 0u);
+          }
+          tc_commit_pair(&done[s], 3);
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (stop) break;
+        tc_commit_pair(&accfull[b], 3);
+      }
+      // no MMA of the pair may be in flight when either CTA frees its TMEM
+      tc_commit_pair(drain, 1);
+      mbar_wait(drain, 0, nullptr, limit_ns, kSiteDrain);
+    }
+  } else if (warp < C::kFirstEpi) {
+    // ---------------- converters (both CTAs) ----------------
+    const int ct = threadIdx.x - 64;
+    uint32_t g = 0;
+    bool stop = false;
+    for (int it = pair; it < nitems && !stop; it += npairs) {
+      int kt, rt, c0, c1, part;
+      item(it, kt, rt, c0, c1, part);
+      for (int c = c0; c < c1; ++c, ++g) {
+        const int s = g % S;
+        const uint32_t sA = smem_u32(smem) + s * C::kStageBytes;
+        const uint32_t raw = sA + TERMS * kGtABytes + C::kBBytes;
+        if constexpr (KIND == kGradInput) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull))) {
+            stop = true;
+            break;
+          }
+          // a quarter-warp takes four words of one 64-k block in two
+          // neighbouring rows: the swizzle puts its eight 16-byte stores on
+          // eight different bank groups
+          const int row0 = 2 * (ct >> 4) + ((ct >> 2) & 1), gw = (ct & 3) + ((ct >> 3) & 1) * 4;
+          constexpr int kRowStep = 32 * C::kConvWarps / 8;
+          uint32_t w[kGtBC / kRowStep];
+#pragma unroll
+          for (int i = 0; i < kGtBC / kRowStep; ++i) w[i] = ld_shared_u32(raw + (row0 + i * kRowStep) * 32 + gw * 4);
+#pragma unroll
+          for (int i = 0; i < kGtBC / kRowStep; ++i) {
+            const int row = row0 + i * kRowStep;
+            uint32_t v[8];
+            expand16(w[i], v);
+            const uint32_t rowa = sA + (gw >> 2) * 8192 + row * 128, ch = 2 * (gw & 3), x = row & 7;
+            st_shared_v4(rowa + ((ch ^ x) << 4), v[0], v[1], v[2], v[3]);
+            st_shared_v4(rowa + (((ch + 1) ^ x) << 4), v[4], v[5], v[6], v[7]);
+          }
+        } else {
+          constexpr int kRowStep = 32 * C::kConvWarps / 16, kUnits = kGtBC / kRowStep;
+          const int row0 = ct >> 4, u = ct & 15;   // 8 codes of a row
+          float sc[kUnits];
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int m = c * kGtBC + row0 + i * kRowStep;
+            sc[i] = m < P.L ? __ldg(P.scale + m) : 1.f;
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull))) {
+            stop = true;
+            break;
+          }
+          uint2 q[kUnits];
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) q[i] = ld_shared_v2(raw + (row0 + i * kRowStep) * 128 + u * 8);
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int row = row0 + i * kRowStep;
+            float r;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc[i]));   // within 2^-23, far below the operand's step
+            uint64_t rr;
+            asm("mov.b64 %0, {%1, %1};" : "=l"(rr) : "f"(r));
+            const uint32_t x0 = q[i].x ^ 0x80808080u, x1 = q[i].y ^ 0x80808080u;
+            uint32_t hi[4], lo[4];
+            split2<TERMS>(codes2_f32<0>(x0, rr), hi[0], lo[0]);
+            split2<TERMS>(codes2_f32<2>(x0, rr), hi[1], lo[1]);
+            split2<TERMS>(codes2_f32<0>(x1, rr), hi[2], lo[2]);
+            split2<TERMS>(codes2_f32<2>(x1, rr), hi[3], lo[3]);
+            const uint32_t at = sA + (u >> 3) * 8192 + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+            st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+            if (TERMS == 2) st_shared_v4(at + kGtABytes, lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) gt_arrive_leader(&ready[s]);
+      }
+    }
+  } else {
+    // ---------------- epilogue (both CTAs) ----------------
+    const int q = warp & 3, half = (warp - C::kFirstEpi) >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    const float f = P.gamma ? *P.gamma : 1.f;
+    uint8_t* so = sOut + (warp - C::kFirstEpi) * C::kOutBytes;
+    int i = 0, buf = 0;
+    for (int it = pair; it < nitems; it += npairs, ++i) {
+      int kt, rt, c0, c1, part;
+      item(it, kt, rt, c0, c1, part);
+      const int b = i & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&accfull[b], (i >> 1) & 1, abort_flag, limit_ns, kSiteAcc) &&
+                                       !*abort_flag))
+        break;
+      tc_fence_after();
+      const int kw = kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32, k = kw + lane;
+      const int r0 = rt * BN + half * C::kHalf;
+      const bool kin = kw < P.K;   // K is a multiple of 64: a warp's 32 k are all inside or all outside
+#pragma unroll 1
+      for (int c = 0; c < C::kHalf; c += C::kChunk) {
+        uint32_t v[32];
+        if (C::kChunk == 32)
+          tmem_ld_32x32b_x32(tmem + lane_base + b * BN + half * C::kHalf + c, v);
+        else
+          tmem_ld_32x32b_x16(tmem + lane_base + b * BN + half * C::kHalf + c, v);
+        tmem_wait_ld();
+        const int r = r0 + c;
+        if (!kin || r >= P.R) continue;
+        if (P.mode == kGtTmaBf16) {
+          uint8_t* tile = so + buf * (C::kOutBytes / 2);
+          buf ^= 1;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // this tile's last store
+          __syncwarp();
+#pragma unroll
+          for (int t = 0; t < C::kChunk; ++t)
+            reinterpret_cast<uint16_t*>(tile)[t * 32 + lane] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[t]) * f));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmD, kw, r, tile);
+            bulk_commit_group();
+          }
+        } else {
+          const size_t o = (static_cast<size_t>(part) * P.R + r) * P.K + k;
+          const int n = min(C::kChunk, P.R - r);
+          const uint32_t ld = static_cast<uint32_t>(P.K);
+          if (P.mode == kGtF32) {
+            float* y = static_cast<float*>(P.out) + o;
+#pragma unroll
+            for (int t = 0; t < C::kChunk; ++t)
+              if (t < n) y[t * ld] = __uint_as_float(v[t]);
+          } else if (P.mode == kGtF32Acc) {
+            float* y = static_cast<float*>(P.out) + o;
+#pragma unroll
+            for (int h = 0; h < C::kChunk; h += 16) {
+              float old[16];
+#pragma unroll
+              for (int t = 0; t < 16; ++t) old[t] = h + t < n ? y[(h + t) * ld] : 0.f;
+#pragma unroll
+              for (int t = 0; t < 16; ++t)
+                if (h + t < n) y[(h + t) * ld] = old[t] + __uint_as_float(v[h + t]);
+            }
+          } else {
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.out) + o;
+#pragma unroll
+            for (int h = 0; h < C::kChunk; h += 16) {
+              float old[16];
+#pragma unroll
+              for (int t = 0; t < 16; ++t) old[t] = h + t < n ? __bfloat162float(y[(h + t) * ld]) : 0.f;
+#pragma unroll
+              for (int t = 0; t < 16; ++t)
+                if (h + t < n) y[(h + t) * ld] = __float2bfloat16_rn(old[t] + __uint_as_float(v[h + t]));
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(&accempty[b], 0);   // accumulator drained
+    }
+    if (lane == 0) bulk_wait_group0();   // outputs written before exit
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();   // the leader has drained its MMAs; both CTAs may free TMEM
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::kTmemCols);
+  }
+}
+
+// out = f * (sum of the parts, in order) (+ out), four elements a thread.
+__global__ void __launch_bounds__(256)
+    bl_grad_join_kernel(const float* __restrict__ part, int splits, size_t n4, const float* __restrict__ gamma,
+                        void* __restrict__ out, int out_bf16, int accumulate) {
+  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const float4* p = reinterpret_cast<const float4*>(part);
+  float4 s = p[i];
+  for (int j = 1; j < splits; ++j) {
+    const float4 t = p[static_cast<size_t>(j) * n4 + i];
+    s.x += t.x;
+    s.y += t.y;
+    s.z += t.z;
+    s.w += t.w;
+  }
+  if (gamma) {
+    const float f = *gamma;
+    s.x *= f;
+    s.y *= f;
+    s.z *= f;
+    s.w *= f;
+  }
+  if (out_bf16) {
+    uint2* y = reinterpret_cast<uint2*>(out) + i;
+    if (accumulate) {
+      const uint2 o = *y;
+      s.x += bf16_lo(o.x);
+      s.y += bf16_hi(o.x);
+      s.z += bf16_lo(o.y);
+      s.w += bf16_hi(o.y);
+    }
+    *y = make_uint2(pack2_bf16(s.x, s.y), pack2_bf16(s.z, s.w));
+  } else {
+    float4* y = reinterpret_cast<float4*>(out) + i;
+    if (accumulate) {
+      const float4 o = *y;
+      s.x += o.x;
+      s.y += o.y;
+      s.z += o.z;
+      s.w += o.w;
+    }
+    *y = s;
+  }
+}
+
+// Rows of dY at a 16-byte stride (TMA needs one): [M, N] -> [M, ld].
+__global__ void __launch_bounds__(256)
+    bl_grad_pad_kernel(const uint16_t* __restrict__ src, uint16_t* __restrict__ dst, int M, int N, int ld) {
+  for (int m = blockIdx.y; m < M; m += gridDim.y)
+    for (int n = blockIdx.x * 256 + threadIdx.x; n < ld; n += gridDim.x * 256)
+      dst[static_cast<size_t>(m) * ld + n] = n < N ? src[static_cast<size_t>(m) * N + n] : 0;
+}
+
+}  // namespace bl
