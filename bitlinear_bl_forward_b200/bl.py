@@ -594,29 +594,44 @@ BL_GRAD_ACCUMULATE = 1
 BL_GRAD_BF16 = 2
 
 
-def _train(t: torch.Tensor, dtype, name: str, shape) -> int:
-    """_dev with the shape checked, on the current device (the one whose
-    stream the call uses)."""
-    p = _dev(t, dtype, name)
-    if tuple(t.shape) != shape:
+def _train(t: torch.Tensor, dtype, name: str, shape, dev: int) -> int:
+    """_dev with the shape checked, on device `dev` (the current one, whose
+    stream the call uses).  The error is looked for only when there is one: a
+    call's host time is what a small pass costs."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev):
+        return t.data_ptr()
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return p
+    raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
-def _packed(Wp: torch.Tensor, N: int, K: int) -> int:
+def _packed(Wp: torch.Tensor, N: int, K: int, dev: int) -> int:
     """Packed weights of any shape with the layer's N*K/4 bytes."""
     p = _dev(Wp, torch.uint8, "Wp")
     if Wp.numel() != N * K // 4:
         raise ValueError(f"Wp must hold {N * K // 4} bytes, got {Wp.numel()}")
+    if Wp.get_device() != dev:
+        raise ValueError(f"Wp is on {Wp.device}, not on the current device")
     return p
 
 
-def _matrix(t: torch.Tensor, name: str):
+def _matrix(t: torch.Tensor, dtype, name: str):
+    """(rows, columns, pointer, device) of a call's leading matrix."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError(f"{name} must be a matrix")
-    return t.shape
+    dev = torch.cuda.current_device() if t.is_cuda else -1
+    return *t.shape, _train(t, dtype, name, t.shape, dev), dev
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(dev: int) -> int:
+    """Handle of device dev's current stream (torch.cuda.current_stream takes
+    3 us to build an object around it)."""
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _ws_args(workspace, need: int, device):
@@ -641,19 +656,18 @@ def bl_forward_checkpoint(X: torch.Tensor, Wp: torch.Tensor, gamma: torch.Tensor
     parameters, that keeps its activations as 8-bit codes: returns (Y bf16
     [M, N], Xq int8 [M, K], scale fp32 [M], stat fp32 [M] or None), what
     bl_backward_weight and bl_norm_backward_checkpoint take."""
-    M, K = _matrix(X, "X")
-    px = _train(X, torch.bfloat16, "X", (M, K))
-    pw = _packed(Wp, N, K)
-    pg = _dev(gamma, torch.float32, "gamma")
+    M, K, px, dev = _matrix(X, torch.bfloat16, "X")
+    pw = _packed(Wp, N, K, dev)
+    pg = _train(gamma, torch.float32, "gamma", gamma.shape, dev)
     nrm = BL_NORM_NONE if norm is None else norm
-    Y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    py = _train(Y, torch.bfloat16, "out", (M, N))
+    Y = out if out is not None else X.new_empty((M, N))
+    py = _train(Y, torch.bfloat16, "out", (M, N), dev)
     Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
     scale = torch.empty(M, dtype=torch.float32, device=X.device)
     stat = torch.empty(M, dtype=torch.float32, device=X.device) if nrm != BL_NORM_NONE else None
     wp, wn, _keep = _ws_args(workspace, lib().bl_forward_checkpoint_workspace_bytes(M, K, N, bits), X.device)
     _check(lib().bl_forward_checkpoint(px, nrm, eps, M, K, N, pw, pg, bits, py, Xq.data_ptr(), scale.data_ptr(),
-                                       stat.data_ptr() if stat is not None else None, wp, wn, _stream()),
+                                       stat.data_ptr() if stat is not None else None, wp, wn, _stream_of(dev)),
            "bl_forward_checkpoint")
     return Y, Xq, scale, stat
 
@@ -666,14 +680,13 @@ def bl_backward_input(dY: torch.Tensor, Wp: torch.Tensor, gamma: torch.Tensor, K
                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """dX = gamma * dY C: bf16 [M, N] output gradients and the packed weights
     [N, K/4] -> bf16 [M, K]."""
-    M, N = _matrix(dY, "dY")
-    py = _train(dY, torch.bfloat16, "dY", (M, N))
-    pw = _packed(Wp, N, K)
-    pg = _dev(gamma, torch.float32, "gamma")
-    dX = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dY.device)
-    px = _train(dX, torch.bfloat16, "out", (M, K))
+    M, N, py, dev = _matrix(dY, torch.bfloat16, "dY")
+    pw = _packed(Wp, N, K, dev)
+    pg = _train(gamma, torch.float32, "gamma", gamma.shape, dev)
+    dX = out if out is not None else dY.new_empty((M, K))
+    px = _train(dX, torch.bfloat16, "out", (M, K), dev)
     wp, wn, _keep = _ws_args(workspace, lib().bl_backward_input_workspace_bytes(M, K, N), dY.device)
-    _check(lib().bl_backward_input(py, M, K, N, pw, pg, px, wp, wn, _stream()), "bl_backward_input")
+    _check(lib().bl_backward_input(py, M, K, N, pw, pg, px, wp, wn, _stream_of(dev)), "bl_backward_input")
     return dX
 
 
@@ -687,21 +700,21 @@ def bl_backward_weight(dY: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, 
     """dW = dY^T (Xq / scale): bf16 [M, N] output gradients and the forward's
     int8 codes [M, K] and scales [M] -> fp32 (or bf16) [N, K].  With `out`,
     its dtype counts; accumulate=True adds to it."""
-    M, N = _matrix(dY, "dY")
-    M2, K = _matrix(Xq, "Xq")
-    py = _train(dY, torch.bfloat16, "dY", (M2, N))
-    pq = _train(Xq, torch.int8, "Xq", (M, K))
-    ps = _train(scale, torch.float32, "scale", (M,))
+    M, N, py, dev = _matrix(dY, torch.bfloat16, "dY")
+    M2, K, pq, _ = _matrix(Xq, torch.int8, "Xq")
+    if M2 != M:
+        raise ValueError(f"dY has {M} rows, Xq {M2}")
+    ps = _train(scale, torch.float32, "scale", (M,), dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = torch.empty((N, K), dtype=dtype, device=dY.device)
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("dW must be float32 or bfloat16")
-    po = _train(out, out.dtype, "out", (N, K))
+    po = _train(out, out.dtype, "out", (N, K), dev)
     flags = (BL_GRAD_ACCUMULATE if accumulate else 0) | (BL_GRAD_BF16 if out.dtype == torch.bfloat16 else 0)
     wp, wn, _keep = _ws_args(workspace, lib().bl_backward_weight_workspace_bytes(M, K, N, flags), dY.device)
-    _check(lib().bl_backward_weight(py, pq, ps, M, K, N, flags, po, wp, wn, _stream()), "bl_backward_weight")
+    _check(lib().bl_backward_weight(py, pq, ps, M, K, N, flags, po, wp, wn, _stream_of(dev)), "bl_backward_weight")
     return out
 
 
@@ -709,16 +722,15 @@ def bl_norm_forward(X: torch.Tensor, norm: int, weight: torch.Tensor | None = No
                     bias: torch.Tensor | None = None, eps: float = 1e-5, out: torch.Tensor | None = None):
     """RMSNorm (BL_NORM_RMS) or LayerNorm (BL_NORM_LAYER) of bf16 [M, K] rows:
     returns (Y bf16 [M, K], mean fp32 [M] or None, stat fp32 [M])."""
-    M, K = _matrix(X, "X")
-    px = _train(X, torch.bfloat16, "X", (M, K))
-    pw = _train(weight, torch.bfloat16, "weight", (K,)) if weight is not None else None
-    pb = _train(bias, torch.bfloat16, "bias", (K,)) if bias is not None else None
+    M, K, px, dev = _matrix(X, torch.bfloat16, "X")
+    pw = _train(weight, torch.bfloat16, "weight", (K,), dev) if weight is not None else None
+    pb = _train(bias, torch.bfloat16, "bias", (K,), dev) if bias is not None else None
     Y = out if out is not None else torch.empty_like(X)
-    py = _train(Y, torch.bfloat16, "out", (M, K))
+    py = _train(Y, torch.bfloat16, "out", (M, K), dev)
     stat = torch.empty(M, dtype=torch.float32, device=X.device)
     mean = torch.empty(M, dtype=torch.float32, device=X.device) if norm == BL_NORM_LAYER else None
     _check(lib().bl_norm_forward(px, pw, pb, norm, eps, M, K, py, mean.data_ptr() if mean is not None else None,
-                                 stat.data_ptr(), _stream()), "bl_norm_forward")
+                                 stat.data_ptr(), _stream_of(dev)), "bl_norm_forward")
     return Y, mean, stat
 
 
@@ -734,27 +746,26 @@ def bl_norm_backward(dY: torch.Tensor, X: torch.Tensor, norm: int, stat: torch.T
     """Gradients of bl_norm_forward: (dX bf16 [M, K], dweight fp32 [K] when
     there is a weight or `dweight`, dbias fp32 [K] when need_bias or `dbias`).
     accumulate=True adds to the given dweight and dbias."""
-    M, K = _matrix(X, "X")
-    px = _train(X, torch.bfloat16, "X", (M, K))
-    py = _train(dY, torch.bfloat16, "dY", (M, K))
-    pst = _train(stat, torch.float32, "stat", (M,))
-    pmu = _train(mean, torch.float32, "mean", (M,)) if mean is not None else None
-    pw = _train(weight, torch.bfloat16, "weight", (K,)) if weight is not None else None
+    M, K, px, dev = _matrix(X, torch.bfloat16, "X")
+    py = _train(dY, torch.bfloat16, "dY", (M, K), dev)
+    pst = _train(stat, torch.float32, "stat", (M,), dev)
+    pmu = _train(mean, torch.float32, "mean", (M,), dev) if mean is not None else None
+    pw = _train(weight, torch.bfloat16, "weight", (K,), dev) if weight is not None else None
     if accumulate and ((weight is not None and dweight is None) or (need_bias and dbias is None)):
         raise ValueError("accumulate needs dweight and dbias")
     if dweight is None and weight is not None:
         dweight = torch.empty(K, dtype=torch.float32, device=X.device)
     if dbias is None and need_bias:
         dbias = torch.empty(K, dtype=torch.float32, device=X.device)
-    pdw = _train(dweight, torch.float32, "dweight", (K,)) if dweight is not None else None
-    pdb = _train(dbias, torch.float32, "dbias", (K,)) if dbias is not None else None
+    pdw = _train(dweight, torch.float32, "dweight", (K,), dev) if dweight is not None else None
+    pdb = _train(dbias, torch.float32, "dbias", (K,), dev) if dbias is not None else None
     dX = out if out is not None else torch.empty_like(X)
-    pdx = _train(dX, torch.bfloat16, "out", (M, K))
+    pdx = _train(dX, torch.bfloat16, "out", (M, K), dev)
     wp, wn, _keep = None, 0, None
     if pdw is not None or pdb is not None:
         wp, wn, _keep = _ws_args(workspace, lib().bl_norm_backward_workspace_bytes(M, K), X.device)
     _check(lib().bl_norm_backward(py, px, pw, norm, eps, pmu, pst, M, K, BL_GRAD_ACCUMULATE if accumulate else 0, pdx,
-                                  pdw, pdb, wp, wn, _stream()), "bl_norm_backward")
+                                  pdw, pdb, wp, wn, _stream_of(dev)), "bl_norm_backward")
     return dX, dweight, dbias
 
 
@@ -763,14 +774,13 @@ def bl_norm_backward_checkpoint(dXn: torch.Tensor, Xq: torch.Tensor, scale: torc
                                 out: torch.Tensor | None = None) -> torch.Tensor:
     """Backward of the norm inside bl_forward_checkpoint from its codes: dXn
     bf16 [M, K] (bl_backward_input), Xq, scale and stat -> dX bf16 [M, K]."""
-    M, K = _matrix(dXn, "dXn")
-    pg = _train(dXn, torch.bfloat16, "dXn", (M, K))
-    pq = _train(Xq, torch.int8, "Xq", (M, K))
-    ps = _train(scale, torch.float32, "scale", (M,))
-    pst = _train(stat, torch.float32, "stat", (M,))
+    M, K, pg, dev = _matrix(dXn, torch.bfloat16, "dXn")
+    pq = _train(Xq, torch.int8, "Xq", (M, K), dev)
+    ps = _train(scale, torch.float32, "scale", (M,), dev)
+    pst = _train(stat, torch.float32, "stat", (M,), dev)
     dX = out if out is not None else torch.empty_like(dXn)
-    px = _train(dX, torch.bfloat16, "out", (M, K))
-    _check(lib().bl_norm_backward_checkpoint(pg, pq, ps, norm, eps, pst, M, K, px, _stream()),
+    px = _train(dX, torch.bfloat16, "out", (M, K), dev)
+    _check(lib().bl_norm_backward_checkpoint(pg, pq, ps, norm, eps, pst, M, K, px, _stream_of(dev)),
            "bl_norm_backward_checkpoint")
     return dX
 

@@ -26,6 +26,12 @@
 // bf16; A's conversion runs beside the MMAs.
 // Few tiles, long sum: the sum is split over pairs; the parts (fp32) meet in
 // bl_grad_join_kernel in a fixed order.
+// The tensor core truncates when it adds to an fp32 accumulator, so the error
+// of a long sum grows with its length instead of its root: 1.0e-5 of the norm
+// over 4096 tokens, where rounding would leave 1e-6 (measured).  An fp32
+// result is therefore summed in segments of 1024 tokens, which the epilogue
+// adds up with rounding: the pair that owns the tile stores the first and adds
+// the others to its own output, which is still in L2.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,6 +46,7 @@ constexpr int kGtBC = 64;                 // rows of the sum a stage
 constexpr int kGtK = 128;                 // k a CTA (256 a pair)
 constexpr int kGtABytes = kGtBC * kGtK * 2;   // one expanded operand tile: two 64-k blocks of 64 rows x 128 bytes
 constexpr int kGtEpiWarps = 8;
+constexpr int kGtSegment = 16;            // stages an fp32 result sums in one accumulator
 
 // TERMS: bf16 terms of A (2: hi + lo).
 template <int KIND, int TERMS, int BN>
@@ -47,22 +54,29 @@ struct GtCfg {
   static constexpr int kHalf = BN / 2;                         // r rows staged per CTA
   static constexpr int kBBytes = kHalf * kGtBC * 2;
   static constexpr int kRawBytes = KIND == kGradInput ? kGtBC * kGtK / 4 : kGtBC * kGtK;
-  static constexpr int kStageBytes = TERMS * kGtABytes + kBBytes + kRawBytes;
-  static constexpr int kConvWarps = KIND == kGradInput ? 4 : 8;
-  static constexpr int kFirstEpi = 2 + kConvWarps;
+  static constexpr int kInBytes = kBBytes + kRawBytes;         // what TMA brings for a stage
+  static constexpr int kASlotBytes = TERMS * kGtABytes;
+  // converter warps work in groups, each on a stage of its own
+  static constexpr int kGroupWarps = KIND == kGradInput ? 4 : 8;
+  static constexpr int kGroups = KIND == kGradInput ? 3 : 2;
+  static constexpr int kFirstEpi = 2 + kGroupWarps * kGroups;
   static constexpr int kThreads = 32 * (kFirstEpi + kGtEpiWarps);
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;       // r of one epilogue step
-  static constexpr int kOutBytes = 2 * kChunk * 64;            // two bf16 staging tiles [r][32 k] a warp
+  static constexpr int kOutBytes = TERMS == 1 ? 2 * kChunk * 64 : 0;   // two bf16 staging tiles [r][32 k] a warp
   static constexpr int kOutTotal = kGtEpiWarps * kOutBytes;
-  static constexpr int kBudget = 227 * 1024 - 1024 - 512 - kOutTotal;
-  static constexpr int kMaxStages = kBudget / kStageBytes;
+  static constexpr int kASlots = kGroups + 1;                  // being expanded, and one being read
+  static constexpr int kBudget = 227 * 1024 - 1024 - 512 - kOutTotal - kASlots * kASlotBytes;
+  static constexpr int kMaxStages = kBudget / kInBytes;
   static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
-  static constexpr int kOutOffset = kStages * kStageBytes;
+  static constexpr int kAOffset = 0;
+  static constexpr int kInOffset = kASlots * kASlotBytes;
+  static constexpr int kSegment = TERMS == 2 ? kGtSegment : 1 << 30;
+  static constexpr int kOutOffset = kInOffset + kStages * kInBytes;
   static constexpr int kBarOffset = kOutOffset + kOutTotal;
   static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
-  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-  static_assert(kStages >= 2 && kSmemBytes <= 227 * 1024, "shared memory");
-  static_assert(kStageBytes % 1024 == 0, "stage tiles are 1024-byte aligned");
+  static constexpr int kTmemCols = 2 * BN <= 64 ? 64 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
+  static_assert(kStages > kASlots && kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(kInBytes % 1024 == 0, "operand tiles are 1024-byte aligned");
   static_assert((3 * kStages + 5) * 8 + 8 <= 512, "barriers");
 };
 
@@ -93,16 +107,49 @@ constexpr uint32_t kGtDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t gt_desc_mn_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | ((8192u >> 4) << 16); }
 __device__ __forceinline__ uint32_t gt_desc_k_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
 
-__device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
-                                                 uint32_t accumulate) {
+// The four MMAs (K = 16 each) of one operand tile, A MN-major (2048 bytes a
+// step) and B a step of BSTEP 16-byte units: one asm block, so that the issuing
+// thread does little else.  The first accumulates when acc0 != 0.
+template <int BSTEP>
+__device__ __forceinline__ void mma_bf16_tile_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                                   uint32_t acc0) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t.reg .b32 a, b;\n\t"
       "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.eq.b32 q, %5, %5;\n\t"
       "mov.b64 da, {%1, %3};\n\t"
       "mov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(kGtDescHi), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t"
+      "add.u32 a, %1, 128;\n\t"
+      "add.u32 b, %2, %6;\n\t"
+      "mov.b64 da, {a, %3};\n\t"
+      "mov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, q;\n\t"
+      "add.u32 a, %1, 256;\n\t"
+      "add.u32 b, %2, %7;\n\t"
+      "mov.b64 da, {a, %3};\n\t"
+      "mov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, q;\n\t"
+      "add.u32 a, %1, 384;\n\t"
+      "add.u32 b, %2, %8;\n\t"
+      "mov.b64 da, {a, %3};\n\t"
+      "mov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, q;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(kGtDescHi), "r"(idesc), "r"(acc0), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP)
       : "memory");
+}
+
+// One lane of a converged warp, chosen by the hardware: the branch it guards
+// stays warp-uniform for the compiler, so the MMA operands live in uniform
+// registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // Arrive on CTA 0's copy of a barrier after generic shared-memory writes that
@@ -208,7 +255,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&done[s], 1);
-      mbar_init(&ready[s], 2 * C::kConvWarps);
+      mbar_init(&ready[s], 2 * C::kGroupWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
@@ -252,13 +299,12 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         for (int c = c0; c < c1; ++c, ++g) {
           const int s = g % S;
           if (g >= static_cast<uint32_t>(S) &&
-              !mbar_wait_cluster(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty)) {
+              !mbar_wait(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty)) {
             stop = true;
             break;
           }
-          uint8_t* st = smem + s * C::kStageBytes;
-          uint8_t* sB = st + TERMS * kGtABytes;
-          mbar_arrive_expect_tx(&full[s], C::kBBytes + C::kRawBytes);
+          uint8_t* sB = smem + C::kInOffset + s * C::kInBytes;
+          mbar_arrive_expect_tx(&full[s], C::kInBytes);
           tma_load_2d(sB + C::kBBytes, &tmA, KIND == kGradInput ? k0 / 4 : k0, c * kGtBC, &full[s]);
           if (KIND == kGradInput) {
             tma_load_2d(sB, &tmB, c * kGtBC, r0, &full[s]);
@@ -276,63 +322,82 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer (leader only) ----------------
-    if (lane == 0 && rank == 0) {
+    // ---------------- MMA issuer (leader only; the whole warp, one lane issues) ----------------
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16(2 * kGtK, BN, KIND == kGradWeight);
+      constexpr uint32_t kBStep = KIND == kGradInput ? 2 : 128;   // 16 of the sum: 32 bytes K-major, 2048 MN-major
       const uint32_t base = smem_u32(smem);
-      int s = 0, i = 0;
+      const uint32_t a0 = gt_desc_mn_lo(base);
+      const uint32_t b0 = KIND == kGradInput ? gt_desc_k_lo(base + C::kInOffset) : gt_desc_mn_lo(base + C::kInOffset);
+      int s = 0, as = 0, i = 0;
       uint32_t ph = 0;
       bool stop = false;
-      for (int it = pair; it < nitems && !stop; it += npairs, ++i) {
+      for (int it = pair; it < nitems && !stop; it += npairs) {
         int kt, rt, c0, c1, part;
         item(it, kt, rt, c0, c1, part);
-        const int b = i & 1;
-        if (i >= 2 && !mbar_wait_cluster(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + b * BN;
-        for (int c = c0; c < c1; ++c) {
-          if (!mbar_wait_cluster(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull)) {
+        while (c0 < c1) {   // a segment: the accumulator that was drained longest ago
+          const int b = i & 1, ce = min(c1, c0 + min(C::kSegment, c1 - c0));
+          if (i >= 2 && !mbar_wait(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc)) {
             stop = true;
             break;
           }
           tc_fence_after();
-          const uint32_t st = base + s * C::kStageBytes, sb = st + TERMS * kGtABytes;
-          const uint32_t blo = KIND == kGradInput ? gt_desc_k_lo(sb) : gt_desc_mn_lo(sb);
-#pragma unroll
-          for (int t = 0; t < TERMS; ++t) {
-            const uint32_t alo = gt_desc_mn_lo(st + t * kGtABytes);
-#pragma unroll
-            for (int k = 0; k < kGtBC / 16; ++k)   // 16 rows of the sum: 2048 bytes MN-major, 32 bytes K-major
-              mma_bf16_ss_pair(d_tmem, alo + k * 128, blo + k * (KIND == kGradInput ? 2 : 128), idesc,
-                               (c != c0 || t != 0 || k != 0) ? 1u : 0u);
+          const uint32_t d_tmem = tmem + b * BN;
+          uint32_t acc = 0;
+          for (; c0 < ce; ++c0) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull))) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t alo = a0 + as * (C::kASlotBytes / 16), blo = b0 + s * (C::kInBytes / 16);
+              mma_bf16_tile_pair<kBStep>(d_tmem, alo, blo, idesc, acc);
+              if (TERMS == 2) mma_bf16_tile_pair<kBStep>(d_tmem, alo + kGtABytes / 16, blo, idesc, 1u);
+              tc_commit_pair(&done[s], 3);
+            }
+            acc = 1;
+            if (++as == C::kASlots) as = 0;
+            if (++s == S) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
-          tc_commit_pair(&done[s], 3);
-          if (++s == S) {
-            s = 0;
-            ph ^= 1u;
-          }
+          if (stop) break;
+          if (elect_one()) tc_commit_pair(&accfull[b], 3);
+          ++i;
         }
-        if (stop) break;
-        tc_commit_pair(&accfull[b], 3);
       }
       // no MMA of the pair may be in flight when either CTA frees its TMEM
-      tc_commit_pair(drain, 1);
+      if (elect_one()) tc_commit_pair(drain, 1);
       mbar_wait(drain, 0, nullptr, limit_ns, kSiteDrain);
     }
   } else if (warp < C::kFirstEpi) {
     // ---------------- converters (both CTAs) ----------------
-    const int ct = threadIdx.x - 64;
+    const int grp = (warp - 2) / C::kGroupWarps;
+    const int ct = threadIdx.x - 64 - grp * 32 * C::kGroupWarps;
     uint32_t g = 0;
     bool stop = false;
     for (int it = pair; it < nitems && !stop; it += npairs) {
       int kt, rt, c0, c1, part;
       item(it, kt, rt, c0, c1, part);
       for (int c = c0; c < c1; ++c, ++g) {
+        if (g % C::kGroups != static_cast<uint32_t>(grp)) continue;
         const int s = g % S;
-        const uint32_t sA = smem_u32(smem) + s * C::kStageBytes;
-        const uint32_t raw = sA + TERMS * kGtABytes + C::kBBytes;
+        const uint32_t sA = smem_u32(smem) + (g % C::kASlots) * C::kASlotBytes;
+        const uint32_t raw = smem_u32(smem) + C::kInOffset + s * C::kInBytes + C::kBBytes;
+        // the raw rows are here, and the MMAs of the stage that last used the
+        // operand slot are done
+        auto wait_stage = [&]() {
+          bool ok = mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull);
+          if (ok && g >= static_cast<uint32_t>(C::kASlots)) {
+            const uint32_t gp = g - C::kASlots;
+            ok = mbar_wait(&done[gp % S], (gp / S) & 1, abort_flag, limit_ns, kSiteExpEmpty);
+          }
+          return __all_sync(0xffffffffu, ok) != 0;
+        };
         if constexpr (KIND == kGradInput) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull))) {
+          if (!wait_stage()) {
             stop = true;
             break;
           }
@@ -340,7 +405,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           // neighbouring rows: the swizzle puts its eight 16-byte stores on
           // eight different bank groups
           const int row0 = 2 * (ct >> 4) + ((ct >> 2) & 1), gw = (ct & 3) + ((ct >> 3) & 1) * 4;
-          constexpr int kRowStep = 32 * C::kConvWarps / 8;
+          constexpr int kRowStep = 32 * C::kGroupWarps / 8;
           uint32_t w[kGtBC / kRowStep];
 #pragma unroll
           for (int i = 0; i < kGtBC / kRowStep; ++i) w[i] = ld_shared_u32(raw + (row0 + i * kRowStep) * 32 + gw * 4);
@@ -354,7 +419,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
             st_shared_v4(rowa + (((ch + 1) ^ x) << 4), v[4], v[5], v[6], v[7]);
           }
         } else {
-          constexpr int kRowStep = 32 * C::kConvWarps / 16, kUnits = kGtBC / kRowStep;
+          constexpr int kRowStep = 32 * C::kGroupWarps / 16, kUnits = kGtBC / kRowStep;
           const int row0 = ct >> 4, u = ct & 15;   // 8 codes of a row
           float sc[kUnits];
 #pragma unroll
@@ -362,7 +427,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
             const int m = c * kGtBC + row0 + i * kRowStep;
             sc[i] = m < P.L ? __ldg(P.scale + m) : 1.f;
           }
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull))) {
+          if (!wait_stage()) {
             stop = true;
             break;
           }
@@ -399,11 +464,13 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     const float f = P.gamma ? *P.gamma : 1.f;
     uint8_t* so = sOut + (warp - C::kFirstEpi) * C::kOutBytes;
     int i = 0, buf = 0;
-    for (int it = pair; it < nitems; it += npairs, ++i) {
-      int kt, rt, c0, c1, part;
-      item(it, kt, rt, c0, c1, part);
+    int kt = 0, rt = 0, c0 = 0, c1 = 0, part = 0;
+    for (int it = pair; it < nitems; ++i) {
+      if (c0 >= c1) item(it, kt, rt, c0, c1, part);
+      // the segments after the first add to what this thread stored itself
+      const int mode = P.mode == kGtF32 && c0 != part * P.per ? kGtF32Acc : P.mode;
       const int b = i & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&accfull[b], (i >> 1) & 1, abort_flag, limit_ns, kSiteAcc) &&
+      if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (i >> 1) & 1, abort_flag, limit_ns, kSiteAcc) &&
                                        !*abort_flag))
         break;
       tc_fence_after();
@@ -420,7 +487,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         tmem_wait_ld();
         const int r = r0 + c;
         if (!kin || r >= P.R) continue;
-        if (P.mode == kGtTmaBf16) {
+        if (mode == kGtTmaBf16) {
           uint8_t* tile = so + buf * (C::kOutBytes / 2);
           buf ^= 1;
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // this tile's last store
@@ -439,12 +506,12 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           const size_t o = (static_cast<size_t>(part) * P.R + r) * P.K + k;
           const int n = min(C::kChunk, P.R - r);
           const uint32_t ld = static_cast<uint32_t>(P.K);
-          if (P.mode == kGtF32) {
+          if (mode == kGtF32) {
             float* y = static_cast<float*>(P.out) + o;
 #pragma unroll
             for (int t = 0; t < C::kChunk; ++t)
               if (t < n) y[t * ld] = __uint_as_float(v[t]);
-          } else if (P.mode == kGtF32Acc) {
+          } else if (mode == kGtF32Acc) {
             float* y = static_cast<float*>(P.out) + o;
 #pragma unroll
             for (int h = 0; h < C::kChunk; h += 16) {
@@ -471,7 +538,9 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(&accempty[b], 0);   // accumulator drained
+      if (lane == 0) gt_arrive_leader(&accempty[b]);   // accumulator drained
+      c0 = min(c1, c0 + min(C::kSegment, c1 - c0));
+      if (c0 >= c1) it += npairs;
     }
     if (lane == 0) bulk_wait_group0();   // outputs written before exit
   }
