@@ -139,9 +139,11 @@ __device__ __forceinline__ void mma_bf16_tile_pair(uint32_t d_tmem, uint32_t a_l
       : "memory");
 }
 
-// One lane of a converged warp, chosen by the hardware: the branch it guards
-// stays warp-uniform for the compiler, so the MMA operands live in uniform
-// registers.
+// One lane of a converged warp, chosen by the hardware (the same one every
+// time): the branch it guards stays warp-uniform for the compiler, so that
+// descriptors, addresses and coordinates live in uniform registers.  Behind a
+// lane == 0 branch four MMAs took 450 clocks to issue and a stage's two TMA
+// loads 490; 512 clocks is the tensor work of a stage.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -285,24 +287,26 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
   };
 
   if (warp == 0) {
-    // ---------------- TMA producer (both CTAs) ----------------
-    if (lane == 0) {
+    // ---------------- TMA producer (both CTAs; the whole warp, one lane issues) ----------------
+    if (elect_one()) {
       prefetch_tmap(&tmA);
       prefetch_tmap(&tmB);
-      uint32_t g = 0;
-      bool stop = false;
-      for (int it = pair; it < nitems && !stop; it += npairs) {
-        int kt, rt, c0, c1, part;
-        item(it, kt, rt, c0, c1, part);
-        const int k0 = kt * 2 * kGtK + static_cast<int>(rank) * kGtK;
-        const int r0 = rt * BN + static_cast<int>(rank) * C::kHalf;
-        for (int c = c0; c < c1; ++c, ++g) {
-          const int s = g % S;
-          if (g >= static_cast<uint32_t>(S) &&
-              !mbar_wait(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty)) {
-            stop = true;
-            break;
-          }
+    }
+    uint32_t g = 0;
+    int s = 0;
+    bool stop = false;
+    for (int it = pair; it < nitems && !stop; it += npairs) {
+      int kt, rt, c0, c1, part;
+      item(it, kt, rt, c0, c1, part);
+      const int k0 = kt * 2 * kGtK + static_cast<int>(rank) * kGtK;
+      const int r0 = rt * BN + static_cast<int>(rank) * C::kHalf;
+      for (int c = c0; c < c1; ++c, ++g) {
+        if (g >= static_cast<uint32_t>(S) &&
+            !__all_sync(0xffffffffu, mbar_wait(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty))) {
+          stop = true;
+          break;
+        }
+        if (elect_one()) {
           uint8_t* sB = smem + C::kInOffset + s * C::kInBytes;
           mbar_arrive_expect_tx(&full[s], C::kInBytes);
           tma_load_2d(sB + C::kBBytes, &tmA, KIND == kGradInput ? k0 / 4 : k0, c * kGtBC, &full[s]);
@@ -314,12 +318,13 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
               tma_load_2d(sB + j * 8192, &tmB, r0 + 64 * j, c * kGtBC, &full[s]);
           }
         }
+        if (++s == S) s = 0;
       }
-      const uint32_t issued = g;
-      for (uint32_t s = 0; s < static_cast<uint32_t>(S) && s < issued; ++s) {
-        const uint32_t last = s + S * ((issued - 1 - s) / S);
-        mbar_wait(&full[s], (last / S) & 1, nullptr, limit_ns, kSiteDrain);
-      }
+    }
+    const uint32_t issued = g;
+    for (uint32_t t = 0; t < static_cast<uint32_t>(S) && t < issued; ++t) {
+      const uint32_t last = t + S * ((issued - 1 - t) / S);
+      mbar_wait(&full[t], (last / S) & 1, nullptr, limit_ns, kSiteDrain);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader only; the whole warp, one lane issues) ----------------
