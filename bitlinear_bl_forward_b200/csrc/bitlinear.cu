@@ -1623,11 +1623,11 @@ GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N) {
   const int64_t R = kind == bl::kGradInput ? M : N, L = kind == bl::kGradInput ? N : M;
   g.bn = R > 128 ? 256 : R > 64 || kind == bl::kGradWeight ? 128 : R > 32 ? 64 : 32;
   const int64_t kt = (K + 2 * bl::kGtK - 1) / (2 * bl::kGtK), rt = (R + g.bn - 1) / g.bn;
-  const int64_t nk = (L + bl::kGtBC - 1) / bl::kGtBC, tiles = kt * rt;
+  const int64_t nk = (L + bl::gt_bc(kind, g.bn) - 1) / bl::gt_bc(kind, g.bn), tiles = kt * rt;
   g.kt = static_cast<int>(kt);
   g.rt = static_cast<int>(rt);
   int64_t splits = 1;
-  if (2 * tiles <= kGradPlanPairs) splits = std::max<int64_t>(1, std::min<int64_t>(kGradPlanPairs / tiles, nk / 4));
+  if (2 * tiles <= kGradPlanPairs) splits = std::max<int64_t>(1, std::min<int64_t>(kGradPlanPairs / tiles, nk * bl::gt_bc(kind, g.bn) / 256));
   g.per = static_cast<int>((nk + splits - 1) / splits);
   g.splits = static_cast<int>((nk + g.per - 1) / g.per);
   g.ld = static_cast<int64_t>(align_up(static_cast<size_t>(N), 8));
@@ -1676,12 +1676,12 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
     P.mode = !a.out_bf16 ? (a.accumulate ? bl::kGtF32Acc : bl::kGtF32) : (a.accumulate ? bl::kGtBf16Acc : bl::kGtTmaBf16);
   }
   const bool ok =
-      (KIND == bl::kGradInput ? encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, N, K / 4, K / 4, bl::kGtBC,
+      (KIND == bl::kGradInput ? encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, N, K / 4, K / 4, C::kBC,
                                           bl::kGtK / 4, CU_TENSOR_MAP_SWIZZLE_NONE)
-                              : encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, M, K, K, bl::kGtBC, bl::kGtK,
+                              : encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, M, K, K, C::kBC, bl::kGtK,
                                           CU_TENSOR_MAP_SWIZZLE_NONE)) &&
       encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, M, N, static_cast<uint64_t>(g.ld) * 2,
-                KIND == bl::kGradInput ? C::kHalf : bl::kGtBC, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+                KIND == bl::kGradInput ? C::kHalf : C::kBC, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return BL_ERR_CUDA;
   if (P.mode == bl::kGtTmaBf16) {
     if (!encode_2d(&tmD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, static_cast<uint64_t>(P.R), K, K * 2, C::kChunk, 32,

@@ -12,7 +12,7 @@
 //
 // A pair of CTAs computes 256 (k) x BN (r) per tile:
 //   * every CTA brings its 128 k of the raw low-bit rows and half of the tile
-//     of dY into shared memory with TMA, 64 rows of the sum a stage;
+//     of dY into shared memory with TMA, 64 or 128 rows of the sum a stage;
 //   * converter warps expand the raw rows to bf16 into the swizzled operand
 //     tile next to them (k contiguous: an MN-major operand, so nothing is
 //     transposed).  C is exact in bf16.  q / s is not: an fp32 result takes it
@@ -42,40 +42,49 @@
 
 namespace bl {
 
-constexpr int kGtBC = 64;                 // rows of the sum a stage
 constexpr int kGtK = 128;                 // k a CTA (256 a pair)
-constexpr int kGtABytes = kGtBC * kGtK * 2;   // one expanded operand tile: two 64-k blocks of 64 rows x 128 bytes
 constexpr int kGtEpiWarps = 8;
-constexpr int kGtSegment = 16;            // stages an fp32 result sums in one accumulator
+constexpr int kGtSegment = 1024;          // terms of the sum an fp32 result takes in one accumulator
+
+// Rows of the sum a stage.  The issuing thread spends about 280 clocks a stage
+// on waiting, committing and counting, while few MMAs are queued: at BN = 128 or
+// less a stage of 64 rows is 256 clocks of tensor work and took 527, so those
+// stages are 128 rows (77 -> 62 us for 128 tokens of a 70B-class layer).  At BN =
+// 256 the deeper ring of 64-row stages wins (93 against 99 us for the 2B down
+// projection), and the weight gradient's operands leave no room for more.
+constexpr int gt_bc(int kind, int bn) { return kind == kGradInput && bn <= 128 ? 128 : 64; }
 
 // TERMS: bf16 terms of A (2: hi + lo).
 template <int KIND, int TERMS, int BN>
 struct GtCfg {
+  static constexpr int kBC = gt_bc(KIND, BN);
   static constexpr int kHalf = BN / 2;                         // r rows staged per CTA
-  static constexpr int kBBytes = kHalf * kGtBC * 2;
-  static constexpr int kRawBytes = KIND == kGradInput ? kGtBC * kGtK / 4 : kGtBC * kGtK;
+  static constexpr int kBBytes = kHalf * kBC * 2;              // K-major: boxes of 64 of the sum; MN-major: of 64 r
+  static constexpr int kRawBytes = KIND == kGradInput ? kBC * kGtK / 4 : kBC * kGtK;
+  static constexpr int kBlockBytes = kBC * 128;                // 64 k of an expanded tile
+  static constexpr int kTileBytes = 2 * kBlockBytes;           // one expanded operand tile
   static constexpr int kInBytes = kBBytes + kRawBytes;         // what TMA brings for a stage
-  static constexpr int kASlotBytes = TERMS * kGtABytes;
+  static constexpr int kASlotBytes = TERMS * kTileBytes;
   // converter warps work in groups, each on a stage of its own
   static constexpr int kGroupWarps = KIND == kGradInput ? 4 : 8;
   static constexpr int kGroups = KIND == kGradInput ? 3 : 2;
   static constexpr int kFirstEpi = 2 + kGroupWarps * kGroups;
   static constexpr int kThreads = 32 * (kFirstEpi + kGtEpiWarps);
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;       // r of one epilogue step
-  static constexpr int kOutBytes = TERMS == 1 ? 2 * kChunk * 64 : 0;   // two bf16 staging tiles [r][32 k] a warp
+  static constexpr int kOutBytes = TERMS == 1 ? kChunk * 64 : 0;   // bf16 staging tile [r][32 k] a warp
   static constexpr int kOutTotal = kGtEpiWarps * kOutBytes;
-  static constexpr int kASlots = kGroups + 1;                  // being expanded, and one being read
+  static constexpr int kASlots = kBC == 128 ? 3 : kGroups + 1;   // being expanded, and one being read
   static constexpr int kBudget = 227 * 1024 - 1024 - 512 - kOutTotal - kASlots * kASlotBytes;
   static constexpr int kMaxStages = kBudget / kInBytes;
   static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
   static constexpr int kAOffset = 0;
   static constexpr int kInOffset = kASlots * kASlotBytes;
-  static constexpr int kSegment = TERMS == 2 ? kGtSegment : 1 << 30;
+  static constexpr int kSegment = TERMS == 2 ? kGtSegment / kBC : 1 << 30;
   static constexpr int kOutOffset = kInOffset + kStages * kInBytes;
   static constexpr int kBarOffset = kOutOffset + kOutTotal;
   static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
   static constexpr int kTmemCols = 2 * BN <= 64 ? 64 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
-  static_assert(kStages > kASlots && kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(kStages >= 2 && kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(kInBytes % 1024 == 0, "operand tiles are 1024-byte aligned");
   static_assert((3 * kStages + 5) * 8 + 8 <= 512, "barriers");
 };
@@ -102,9 +111,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool b_mn) {
 
 // High words of the operand descriptors (128-byte swizzle, 8-row atoms 1024
 // bytes apart); the low word is the start address and, for MN-major operands,
-// the 8192 bytes between blocks of 64 elements.
+// the bytes between blocks of 64 elements.
 constexpr uint32_t kGtDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t gt_desc_mn_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | ((8192u >> 4) << 16); }
+__device__ __forceinline__ uint32_t gt_desc_mn_lo(uint32_t addr, uint32_t block_bytes) {
+  return ((addr >> 4) & 0x3FFFu) | ((block_bytes >> 4) << 16);
+}
 __device__ __forceinline__ uint32_t gt_desc_k_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
 
 // The four MMAs (K = 16 each) of one operand tile, A MN-major (2048 bytes a
@@ -137,6 +148,19 @@ __device__ __forceinline__ void mma_bf16_tile_pair(uint32_t d_tmem, uint32_t a_l
       "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, q;\n\t}" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(kGtDescHi), "r"(idesc), "r"(acc0), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP)
       : "memory");
+}
+
+// Whether the phase has completed, without waiting for it.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // One lane of a converged warp, chosen by the hardware (the same one every
@@ -250,7 +274,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int nk = (P.L + kGtBC - 1) / kGtBC;
+  const int nk = (P.L + C::kBC - 1) / C::kBC;
   const int nitems = P.kt * P.rt * P.splits;
 
   if (threadIdx.x == 0) {
@@ -309,13 +333,15 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         if (elect_one()) {
           uint8_t* sB = smem + C::kInOffset + s * C::kInBytes;
           mbar_arrive_expect_tx(&full[s], C::kInBytes);
-          tma_load_2d(sB + C::kBBytes, &tmA, KIND == kGradInput ? k0 / 4 : k0, c * kGtBC, &full[s]);
+          tma_load_2d(sB + C::kBBytes, &tmA, KIND == kGradInput ? k0 / 4 : k0, c * C::kBC, &full[s]);
           if (KIND == kGradInput) {
-            tma_load_2d(sB, &tmB, c * kGtBC, r0, &full[s]);
+#pragma unroll
+            for (int j = 0; j < C::kBC / 64; ++j)
+              tma_load_2d(sB + j * C::kHalf * 128, &tmB, c * C::kBC + 64 * j, r0, &full[s]);
           } else {
 #pragma unroll
             for (int j = 0; j < C::kHalf / 64; ++j)
-              tma_load_2d(sB + j * 8192, &tmB, r0 + 64 * j, c * kGtBC, &full[s]);
+              tma_load_2d(sB + j * C::kBlockBytes, &tmB, r0 + 64 * j, c * C::kBC, &full[s]);
           }
         }
         if (++s == S) s = 0;
@@ -332,11 +358,12 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       constexpr uint32_t idesc = idesc_bf16(2 * kGtK, BN, KIND == kGradWeight);
       constexpr uint32_t kBStep = KIND == kGradInput ? 2 : 128;   // 16 of the sum: 32 bytes K-major, 2048 MN-major
       const uint32_t base = smem_u32(smem);
-      const uint32_t a0 = gt_desc_mn_lo(base);
-      const uint32_t b0 = KIND == kGradInput ? gt_desc_k_lo(base + C::kInOffset) : gt_desc_mn_lo(base + C::kInOffset);
+      const uint32_t a0 = gt_desc_mn_lo(base, C::kBlockBytes);
+      const uint32_t b0 = KIND == kGradInput ? gt_desc_k_lo(base + C::kInOffset)
+                                             : gt_desc_mn_lo(base + C::kInOffset, C::kBlockBytes);
       int s = 0, as = 0, i = 0;
       uint32_t ph = 0;
-      bool stop = false;
+      bool stop = false, seen = false;
       for (int it = pair; it < nitems && !stop; it += npairs) {
         int kt, rt, c0, c1, part;
         item(it, kt, rt, c0, c1, part);
@@ -350,15 +377,25 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           const uint32_t d_tmem = tmem + b * BN;
           uint32_t acc = 0;
           for (; c0 < ce; ++c0) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull))) {
+            if (!__all_sync(0xffffffffu, seen) && !mbar_wait(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull)) {
               stop = true;
               break;
             }
             tc_fence_after();
+            // look at the next stage's barrier now: the answer arrives while
+            // this stage's MMAs are issued (a look that succeeds takes 165
+            // clocks beside the converters' shared-memory traffic)
+            const int sn = s + 1 == S ? 0 : s + 1;
+            seen = mbar_test_wait(&ready[sn], sn ? ph : ph ^ 1u);
             if (elect_one()) {
               const uint32_t alo = a0 + as * (C::kASlotBytes / 16), blo = b0 + s * (C::kInBytes / 16);
-              mma_bf16_tile_pair<kBStep>(d_tmem, alo, blo, idesc, acc);
-              if (TERMS == 2) mma_bf16_tile_pair<kBStep>(d_tmem, alo + kGtABytes / 16, blo, idesc, 1u);
+#pragma unroll
+              for (int j = 0; j < TERMS * (C::kBC / 64); ++j) {   // 64 of the sum each: hi, then lo
+                constexpr int kB = C::kBC / 64;
+                const uint32_t aj = (j / kB) * (C::kTileBytes / 16) + (j % kB) * 512;
+                const uint32_t bj = (j % kB) * (KIND == kGradInput ? C::kHalf * 128 / 16 : 512);
+                mma_bf16_tile_pair<kBStep>(d_tmem, alo + aj, blo + bj, idesc, j ? 1u : acc);
+              }
               tc_commit_pair(&done[s], 3);
             }
             acc = 1;
@@ -395,7 +432,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         // operand slot are done
         auto wait_stage = [&]() {
           bool ok = mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull);
-          if (ok && g >= static_cast<uint32_t>(C::kASlots)) {
+          // (with no more stages than slots the producer has waited for that)
+          if (C::kASlots < S && ok && g >= static_cast<uint32_t>(C::kASlots)) {
             const uint32_t gp = g - C::kASlots;
             ok = mbar_wait(&done[gp % S], (gp / S) & 1, abort_flag, limit_ns, kSiteExpEmpty);
           }
@@ -411,25 +449,25 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           // eight different bank groups
           const int row0 = 2 * (ct >> 4) + ((ct >> 2) & 1), gw = (ct & 3) + ((ct >> 3) & 1) * 4;
           constexpr int kRowStep = 32 * C::kGroupWarps / 8;
-          uint32_t w[kGtBC / kRowStep];
+          uint32_t w[C::kBC / kRowStep];
 #pragma unroll
-          for (int i = 0; i < kGtBC / kRowStep; ++i) w[i] = ld_shared_u32(raw + (row0 + i * kRowStep) * 32 + gw * 4);
+          for (int i = 0; i < C::kBC / kRowStep; ++i) w[i] = ld_shared_u32(raw + (row0 + i * kRowStep) * 32 + gw * 4);
 #pragma unroll
-          for (int i = 0; i < kGtBC / kRowStep; ++i) {
+          for (int i = 0; i < C::kBC / kRowStep; ++i) {
             const int row = row0 + i * kRowStep;
             uint32_t v[8];
             expand16(w[i], v);
-            const uint32_t rowa = sA + (gw >> 2) * 8192 + row * 128, ch = 2 * (gw & 3), x = row & 7;
+            const uint32_t rowa = sA + (gw >> 2) * C::kBlockBytes + row * 128, ch = 2 * (gw & 3), x = row & 7;
             st_shared_v4(rowa + ((ch ^ x) << 4), v[0], v[1], v[2], v[3]);
             st_shared_v4(rowa + (((ch + 1) ^ x) << 4), v[4], v[5], v[6], v[7]);
           }
         } else {
-          constexpr int kRowStep = 32 * C::kGroupWarps / 16, kUnits = kGtBC / kRowStep;
+          constexpr int kRowStep = 32 * C::kGroupWarps / 16, kUnits = C::kBC / kRowStep;
           const int row0 = ct >> 4, u = ct & 15;   // 8 codes of a row
           float sc[kUnits];
 #pragma unroll
           for (int i = 0; i < kUnits; ++i) {
-            const int m = c * kGtBC + row0 + i * kRowStep;
+            const int m = c * C::kBC + row0 + i * kRowStep;
             sc[i] = m < P.L ? __ldg(P.scale + m) : 1.f;
           }
           if (!wait_stage()) {
@@ -452,9 +490,9 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
             split2<TERMS>(codes2_f32<2>(x0, rr), hi[1], lo[1]);
             split2<TERMS>(codes2_f32<0>(x1, rr), hi[2], lo[2]);
             split2<TERMS>(codes2_f32<2>(x1, rr), hi[3], lo[3]);
-            const uint32_t at = sA + (u >> 3) * 8192 + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+            const uint32_t at = sA + (u >> 3) * C::kBlockBytes + row * 128 + (((u & 7) ^ (row & 7)) << 4);
             st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-            if (TERMS == 2) st_shared_v4(at + kGtABytes, lo[0], lo[1], lo[2], lo[3]);
+            if (TERMS == 2) st_shared_v4(at + C::kTileBytes, lo[0], lo[1], lo[2], lo[3]);
           }
         }
         fence_proxy_async_smem();
@@ -468,7 +506,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float f = P.gamma ? *P.gamma : 1.f;
     uint8_t* so = sOut + (warp - C::kFirstEpi) * C::kOutBytes;
-    int i = 0, buf = 0;
+    int i = 0;
     int kt = 0, rt = 0, c0 = 0, c1 = 0, part = 0;
     for (int it = pair; it < nitems; ++i) {
       if (c0 >= c1) item(it, kt, rt, c0, c1, part);
@@ -493,9 +531,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         const int r = r0 + c;
         if (!kin || r >= P.R) continue;
         if (mode == kGtTmaBf16) {
-          uint8_t* tile = so + buf * (C::kOutBytes / 2);
-          buf ^= 1;
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // this tile's last store
+          uint8_t* tile = so;
+          if (lane == 0) bulk_wait_group_read0();   // the last store has read the tile
           __syncwarp();
 #pragma unroll
           for (int t = 0; t < C::kChunk; ++t)
