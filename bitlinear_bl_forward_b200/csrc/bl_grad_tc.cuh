@@ -44,7 +44,7 @@ namespace bl {
 
 constexpr int kGtK = 128;                 // k a CTA (256 a pair)
 constexpr int kGtEpiWarps = 8;
-constexpr int kGtSegment = 1024;          // terms of the sum an fp32 result takes in one accumulator
+constexpr int kGtSegment = 2048;          // terms of the sum an fp32 result takes in one accumulator
 
 // Rows of the sum a stage.  The issuing thread spends about 280 clocks a stage
 // on waiting, committing and counting, while few MMAs are queued: at BN = 128 or
@@ -65,15 +65,20 @@ struct GtCfg {
   static constexpr int kTileBytes = 2 * kBlockBytes;           // one expanded operand tile
   static constexpr int kInBytes = kBBytes + kRawBytes;         // what TMA brings for a stage
   static constexpr int kASlotBytes = TERMS * kTileBytes;
-  // converter warps work in groups, each on a stage of its own
-  static constexpr int kGroupWarps = KIND == kGradInput ? 4 : 8;
-  static constexpr int kGroups = KIND == kGradInput ? 3 : 2;
+  // Converter warps work in groups of four, each group on a stage of its own,
+  // so that a stage's latency (waits, loads, conversion, proxy fence, arrival:
+  // about 1000 clocks) overlaps the others'.  Measured on the 2B layers with 2,
+  // 3 and 4 groups: input 97, 91, - us; weight fp32 191, 191, 193; weight bf16
+  // 162, 150, 143 (half the tensor work beside the same loads); eight warps a
+  // group are slower (fp32 193, bf16 157).
+  static constexpr int kGroupWarps = 4;
+  static constexpr int kGroups = KIND == kGradInput || TERMS == 2 ? 3 : 4;
   static constexpr int kFirstEpi = 2 + kGroupWarps * kGroups;
   static constexpr int kThreads = 32 * (kFirstEpi + kGtEpiWarps);
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;       // r of one epilogue step
   static constexpr int kOutBytes = TERMS == 1 ? kChunk * 64 : 0;   // bf16 staging tile [r][32 k] a warp
   static constexpr int kOutTotal = kGtEpiWarps * kOutBytes;
-  static constexpr int kASlots = kBC == 128 ? 3 : kGroups + 1;   // being expanded, and one being read
+  static constexpr int kASlots = kBC == 128 || TERMS == 2 ? 3 : 4;   // being expanded, and one being read
   static constexpr int kBudget = 227 * 1024 - 1024 - 512 - kOutTotal - kASlots * kASlotBytes;
   static constexpr int kMaxStages = kBudget / kInBytes;
   static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
@@ -191,6 +196,12 @@ __device__ __forceinline__ void gt_arrive_leader(uint64_t* bar) {
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Add to global memory without reading it back (rounds to nearest).  Every
+// output element has one thread that adds to it, in order, so the result does
+// not depend on the run.
+__device__ __forceinline__ void red_add_f32(float* p, float v) {
+  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
@@ -556,14 +567,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           } else if (mode == kGtF32Acc) {
             float* y = static_cast<float*>(P.out) + o;
 #pragma unroll
-            for (int h = 0; h < C::kChunk; h += 16) {
-              float old[16];
-#pragma unroll
-              for (int t = 0; t < 16; ++t) old[t] = h + t < n ? y[(h + t) * ld] : 0.f;
-#pragma unroll
-              for (int t = 0; t < 16; ++t)
-                if (h + t < n) y[(h + t) * ld] = old[t] + __uint_as_float(v[h + t]);
-            }
+            for (int t = 0; t < C::kChunk; ++t)
+              if (t < n) red_add_f32(y + t * ld, __uint_as_float(v[t]));
           } else {
             __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.out) + o;
 #pragma unroll
