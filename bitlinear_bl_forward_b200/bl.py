@@ -617,6 +617,14 @@ def _packed(Wp: torch.Tensor, N: int, K: int, dev: int) -> int:
     return p
 
 
+def _scalar(t: torch.Tensor, name: str, dev: int) -> int:
+    """One fp32 value on the current device, of any shape."""
+    p = _dev(t, torch.float32, name)
+    if t.numel() != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be one value on the current device")
+    return p
+
+
 def _matrix(t: torch.Tensor, dtype, name: str):
     """(rows, columns, pointer, device) of a call's leading matrix."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -658,10 +666,10 @@ def bl_forward_checkpoint(X: torch.Tensor, Wp: torch.Tensor, gamma: torch.Tensor
     bl_backward_weight and bl_norm_backward_checkpoint take."""
     M, K, px, dev = _matrix(X, torch.bfloat16, "X")
     pw = _packed(Wp, N, K, dev)
-    pg = _train(gamma, torch.float32, "gamma", gamma.shape, dev)
+    pg = _scalar(gamma, "gamma", dev)
     nrm = BL_NORM_NONE if norm is None else norm
     Y = out if out is not None else X.new_empty((M, N))
-    py = _train(Y, torch.bfloat16, "out", (M, N), dev)
+    py = Y.data_ptr() if out is None else _train(Y, torch.bfloat16, "out", (M, N), dev)
     Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
     scale = torch.empty(M, dtype=torch.float32, device=X.device)
     stat = torch.empty(M, dtype=torch.float32, device=X.device) if nrm != BL_NORM_NONE else None
@@ -682,9 +690,9 @@ def bl_backward_input(dY: torch.Tensor, Wp: torch.Tensor, gamma: torch.Tensor, K
     [N, K/4] -> bf16 [M, K]."""
     M, N, py, dev = _matrix(dY, torch.bfloat16, "dY")
     pw = _packed(Wp, N, K, dev)
-    pg = _train(gamma, torch.float32, "gamma", gamma.shape, dev)
+    pg = _scalar(gamma, "gamma", dev)
     dX = out if out is not None else dY.new_empty((M, K))
-    px = _train(dX, torch.bfloat16, "out", (M, K), dev)
+    px = dX.data_ptr() if out is None else _train(dX, torch.bfloat16, "out", (M, K), dev)
     wp, wn, _keep = _ws_args(workspace, lib().bl_backward_input_workspace_bytes(M, K, N), dY.device)
     _check(lib().bl_backward_input(py, M, K, N, pw, pg, px, wp, wn, _stream_of(dev)), "bl_backward_input")
     return dX
@@ -705,13 +713,15 @@ def bl_backward_weight(dY: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, 
     if M2 != M:
         raise ValueError(f"dY has {M} rows, Xq {M2}")
     ps = _train(scale, torch.float32, "scale", (M,), dev)
+    if (dtype if out is None else out.dtype) not in (torch.float32, torch.bfloat16):
+        raise TypeError("dW must be float32 or bfloat16")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = torch.empty((N, K), dtype=dtype, device=dY.device)
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("dW must be float32 or bfloat16")
-    po = _train(out, out.dtype, "out", (N, K), dev)
+        po = out.data_ptr()
+    else:
+        po = _train(out, out.dtype, "out", (N, K), dev)
     flags = (BL_GRAD_ACCUMULATE if accumulate else 0) | (BL_GRAD_BF16 if out.dtype == torch.bfloat16 else 0)
     wp, wn, _keep = _ws_args(workspace, lib().bl_backward_weight_workspace_bytes(M, K, N, flags), dY.device)
     _check(lib().bl_backward_weight(py, pq, ps, M, K, N, flags, po, wp, wn, _stream_of(dev)), "bl_backward_weight")
@@ -726,7 +736,7 @@ def bl_norm_forward(X: torch.Tensor, norm: int, weight: torch.Tensor | None = No
     pw = _train(weight, torch.bfloat16, "weight", (K,), dev) if weight is not None else None
     pb = _train(bias, torch.bfloat16, "bias", (K,), dev) if bias is not None else None
     Y = out if out is not None else torch.empty_like(X)
-    py = _train(Y, torch.bfloat16, "out", (M, K), dev)
+    py = Y.data_ptr() if out is None else _train(Y, torch.bfloat16, "out", (M, K), dev)
     stat = torch.empty(M, dtype=torch.float32, device=X.device)
     mean = torch.empty(M, dtype=torch.float32, device=X.device) if norm == BL_NORM_LAYER else None
     _check(lib().bl_norm_forward(px, pw, pb, norm, eps, M, K, py, mean.data_ptr() if mean is not None else None,
@@ -760,7 +770,7 @@ def bl_norm_backward(dY: torch.Tensor, X: torch.Tensor, norm: int, stat: torch.T
     pdw = _train(dweight, torch.float32, "dweight", (K,), dev) if dweight is not None else None
     pdb = _train(dbias, torch.float32, "dbias", (K,), dev) if dbias is not None else None
     dX = out if out is not None else torch.empty_like(X)
-    pdx = _train(dX, torch.bfloat16, "out", (M, K), dev)
+    pdx = dX.data_ptr() if out is None else _train(dX, torch.bfloat16, "out", (M, K), dev)
     wp, wn, _keep = None, 0, None
     if pdw is not None or pdb is not None:
         wp, wn, _keep = _ws_args(workspace, lib().bl_norm_backward_workspace_bytes(M, K), X.device)
@@ -779,7 +789,7 @@ def bl_norm_backward_checkpoint(dXn: torch.Tensor, Xq: torch.Tensor, scale: torc
     ps = _train(scale, torch.float32, "scale", (M,), dev)
     pst = _train(stat, torch.float32, "stat", (M,), dev)
     dX = out if out is not None else torch.empty_like(dXn)
-    px = _train(dX, torch.bfloat16, "out", (M, K), dev)
+    px = dX.data_ptr() if out is None else _train(dX, torch.bfloat16, "out", (M, K), dev)
     _check(lib().bl_norm_backward_checkpoint(pg, pq, ps, norm, eps, pst, M, K, px, _stream_of(dev)),
            "bl_norm_backward_checkpoint")
     return dX

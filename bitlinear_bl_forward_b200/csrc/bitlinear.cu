@@ -1618,18 +1618,45 @@ struct GradPlan {
 
 constexpr int kGradPlanPairs = 74;   // CTA pairs of a B200
 
-GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N) {
+// Tiles of 256 k by bn r on 74 CTA pairs, and the number of parts of the sum:
+// whichever takes least by this model of the kernel (us, measured at full
+// waves): a stage costs (bn + f) / (256 + f) of its time at bn = 256 (tensor
+// work plus what a stage costs anyway: f = 48, or 128 with the weight gradient's
+// conversions), pairs work in waves of whole items, and parts are written and
+// read once more and need a second launch.  What it decides,
+// measured: 4096 x 2560 of a 2B layer's input gradient at bn = 192 (three waves
+// of 220 tiles, 101 us) instead of 256 (three of 160, 132 us); its weight
+// gradient at 256 (four waves, 193 us) instead of 192 (five, 199 us).
+GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N, bool bf16_out) {
   GradPlan g = {};
   const int64_t R = kind == bl::kGradInput ? M : N, L = kind == bl::kGradInput ? N : M;
-  g.bn = R > 128 ? 256 : R > 64 || kind == bl::kGradWeight ? 128 : R > 32 ? 64 : 32;
-  const int64_t kt = (K + 2 * bl::kGtK - 1) / (2 * bl::kGtK), rt = (R + g.bn - 1) / g.bn;
-  const int64_t nk = (L + bl::gt_bc(kind, g.bn) - 1) / bl::gt_bc(kind, g.bn), tiles = kt * rt;
+  const int64_t kt = (K + 2 * bl::kGtK - 1) / (2 * bl::kGtK);
+  const double t256 = kind == bl::kGradInput ? 0.38 : bf16_out ? 0.45 : 0.75;   // 64 rows of the sum
+  const double fixed = kind == bl::kGradInput ? 48 : 128;
+  const int bns[5] = {256, 192, 128, 64, 32};
+  double best = 1e300;
+  for (int b = 0; b < (kind == bl::kGradInput ? 5 : 3); ++b) {
+    const int bn = bns[b], bc = bl::gt_bc(kind, bn);
+    const int64_t rt = (R + bn - 1) / bn, tiles = kt * rt, nk = (L + bc - 1) / bc;
+    const double stage = t256 * (bn + fixed) / (256 + fixed) * (bc / 64);
+    const int64_t fill = std::max<int64_t>(1, kGradPlanPairs / tiles);
+    const int64_t tries[6] = {1, 2, 3, 4, fill, 2 * fill};
+    for (int j = 0; j < (tiles > 4 * kGradPlanPairs ? 1 : 6); ++j) {
+      const int64_t want = std::min<int64_t>(tries[j], std::max<int64_t>(1, nk / 2));
+      const int64_t per = (nk + want - 1) / want, splits = (nk + per - 1) / per;
+      const int64_t waves = (tiles * splits + kGradPlanPairs - 1) / kGradPlanPairs;
+      double t = static_cast<double>(waves) * (static_cast<double>(per) * stage + 0.5);
+      if (splits > 1) t += 2.5 + static_cast<double>(splits) * R * K * 8 / 5e6;
+      if (t < best) {
+        best = t;
+        g.bn = bn;
+        g.rt = static_cast<int>(rt);
+        g.per = static_cast<int>(per);
+        g.splits = static_cast<int>(splits);
+      }
+    }
+  }
   g.kt = static_cast<int>(kt);
-  g.rt = static_cast<int>(rt);
-  int64_t splits = 1;
-  if (2 * tiles <= kGradPlanPairs) splits = std::max<int64_t>(1, std::min<int64_t>(kGradPlanPairs / tiles, nk * bl::gt_bc(kind, g.bn) / 256));
-  g.per = static_cast<int>((nk + splits - 1) / splits);
-  g.splits = static_cast<int>((nk + g.per - 1) / g.per);
   g.ld = static_cast<int64_t>(align_up(static_cast<size_t>(N), 8));
   g.pad_bytes = g.ld == N ? 0 : align_up(static_cast<size_t>(M) * g.ld * 2, 256);
   g.part_bytes = g.splits > 1 ? static_cast<size_t>(g.splits) * R * K * sizeof(float) : 0;
@@ -1713,7 +1740,7 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
 
 template <int KIND>
 bl_status launch_grad(const bl::GradArgs& a, void* workspace, cudaStream_t stream) {
-  const GradPlan g = plan_grad(KIND, a.M, a.K, a.N);
+  const GradPlan g = plan_grad(KIND, a.M, a.K, a.N, a.out_bf16 != 0);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const uint16_t* dY = a.dY;
   bl_status st;
@@ -1730,14 +1757,21 @@ bl_status launch_grad(const bl::GradArgs& a, void* workspace, cudaStream_t strea
       case 32: st = launch_grad_t<KIND, 1, 32>(a, g, dY, parts, stream); break;
       case 64: st = launch_grad_t<KIND, 1, 64>(a, g, dY, parts, stream); break;
       case 128: st = launch_grad_t<KIND, 1, 128>(a, g, dY, parts, stream); break;
+      case 192: st = launch_grad_t<KIND, 1, 192>(a, g, dY, parts, stream); break;
       default: st = launch_grad_t<KIND, 1, 256>(a, g, dY, parts, stream); break;
     }
   } else if (a.out_bf16) {
-    st = g.bn == 128 ? launch_grad_t<KIND, 1, 128>(a, g, dY, parts, stream)
-                     : launch_grad_t<KIND, 1, 256>(a, g, dY, parts, stream);
+    switch (g.bn) {
+      case 128: st = launch_grad_t<KIND, 1, 128>(a, g, dY, parts, stream); break;
+      case 192: st = launch_grad_t<KIND, 1, 192>(a, g, dY, parts, stream); break;
+      default: st = launch_grad_t<KIND, 1, 256>(a, g, dY, parts, stream); break;
+    }
   } else {
-    st = g.bn == 128 ? launch_grad_t<KIND, 2, 128>(a, g, dY, parts, stream)
-                     : launch_grad_t<KIND, 2, 256>(a, g, dY, parts, stream);
+    switch (g.bn) {
+      case 128: st = launch_grad_t<KIND, 2, 128>(a, g, dY, parts, stream); break;
+      case 192: st = launch_grad_t<KIND, 2, 192>(a, g, dY, parts, stream); break;
+      default: st = launch_grad_t<KIND, 2, 256>(a, g, dY, parts, stream); break;
+    }
   }
   if (st != BL_OK || g.splits == 1) return st;
   const size_t n4 = static_cast<size_t>(KIND == bl::kGradInput ? a.M : a.N) * a.K / 4;
@@ -1768,22 +1802,51 @@ bl_status launch_norm_fwd(const uint16_t* X, const uint16_t* w, const uint16_t* 
 // Row gradients only.
 template <bool LAYER, bool CKPT>
 bl_status launch_norm_dx(const bl::NormGradArgs& a, cudaStream_t stream) {
+  if (a.K > bl::kNgRowMaxK) {
+    bl::bl_norm_dx_wide_kernel<LAYER, CKPT><<<a.M, 1024, 0, stream>>>(a);
+    return last_cuda();
+  }
   const int c = row_chunks(a.K), t = row_threads(a.K, c);
   switch (c) {
-    case 1: bl::bl_norm_bwd_kernel<1, LAYER, CKPT, false><<<a.M, t, 0, stream>>>(a); break;
-    case 2: bl::bl_norm_bwd_kernel<2, LAYER, CKPT, false><<<a.M, t, 0, stream>>>(a); break;
-    case 4: bl::bl_norm_bwd_kernel<4, LAYER, CKPT, false><<<a.M, t, 0, stream>>>(a); break;
-    default: bl::bl_norm_bwd_kernel<8, LAYER, CKPT, false><<<a.M, t, 0, stream>>>(a); break;
+    case 1: bl::bl_norm_dx_kernel<1, LAYER, CKPT><<<a.M, t, 0, stream>>>(a); break;
+    case 2: bl::bl_norm_dx_kernel<2, LAYER, CKPT><<<a.M, t, 0, stream>>>(a); break;
+    default: bl::bl_norm_dx_kernel<4, LAYER, CKPT><<<a.M, t, 0, stream>>>(a); break;
   }
   return last_cuda();
 }
 
-// Partial rows of dweight / dbias: one a CTA for rows that fit registers; for
-// wide rows enough row ranges to fill the GPU with the columns' CTAs.
+// The backward with weight gradients, rows of up to 8192: chunks a thread, rows
+// a step, groups a CTA, stages of a group's ring.
+struct NormShape {
+  int c, r, g, st;
+};
+inline NormShape norm_shape(int64_t K) {
+  return K <= 2560 ? NormShape{1, 2, 2, 4} : K <= 5120 ? NormShape{2, 1, 2, 4} : NormShape{2, 1, 1, 6};
+}
+
+// Partial rows of dweight / dbias.  Rows of up to 8192: one a CTA, as many CTAs
+// an SM as shared memory and threads allow.  Wide rows: enough row ranges to
+// fill the GPU with the columns' CTAs.
 inline int norm_parts(int64_t M, int64_t K) {
-  if (K <= bl::kNgRowMaxK) return static_cast<int>(std::min<int64_t>(M, bl::kNgMaxParts));
+  if (K <= bl::kNgRowMaxK) {
+    const NormShape n = norm_shape(K);
+    const int smem = n.g * n.st * n.r * 2 * static_cast<int>(K) * 2 + 2048;
+    const int threads = n.g * row_threads(static_cast<int>(K), n.c);
+    const int occ = std::max(1, std::min(220 * 1024 / smem, 1280 / threads));
+    return static_cast<int>(std::min<int64_t>((M + n.r * n.g - 1) / (n.r * n.g), occ * bl::kNgSms));
+  }
   const int64_t want = std::max<int64_t>(1, (int64_t(1184) * 1024) / K);
   return static_cast<int>(std::min<int64_t>((M + 7) / 8, want));
+}
+
+template <int C, int R, int G, int ST, bool LAYER>
+bl_status launch_norm_rows(const bl::NormGradArgs& a, int parts, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto kern = bl::bl_norm_bwd_kernel<C, R, G, ST, LAYER>;
+  if (!ensure_smem(kern, 200 * 1024, &done)) return BL_ERR_CUDA;
+  const unsigned long long lim = kWaitLimitNs;
+  kern<<<parts, G * row_threads(a.K, C), G * ST * R * 2 * a.K * 2, stream>>>(a, lim);
+  return last_cuda();
 }
 
 template <bool LAYER>
@@ -1791,13 +1854,14 @@ bl_status launch_norm_bwd(bl::NormGradArgs a, float* dweight, float* dbias, int 
   if (!dweight && !dbias) return launch_norm_dx<LAYER, false>(a, stream);
   bl_status st;
   int parts = norm_parts(a.M, a.K);
+  a.want_w = dweight != nullptr;
+  a.want_b = dbias != nullptr;
+  a.part_cols = a.K * (a.want_w + a.want_b);
   if (a.K <= bl::kNgRowMaxK) {
-    const int c = a.K <= 4096 ? 1 : 2, t = row_threads(a.K, c);
-    if (c == 1)
-      bl::bl_norm_bwd_kernel<1, LAYER, false, true><<<parts, t, 0, stream>>>(a);
-    else
-      bl::bl_norm_bwd_kernel<2, LAYER, false, true><<<parts, t, 0, stream>>>(a);
-    if ((st = last_cuda()) != BL_OK) return st;
+    st = a.K <= 2560   ? launch_norm_rows<1, 2, 2, 4, LAYER>(a, parts, stream)
+         : a.K <= 5120 ? launch_norm_rows<2, 1, 2, 4, LAYER>(a, parts, stream)
+                       : launch_norm_rows<2, 1, 1, 6, LAYER>(a, parts, stream);
+    if (st != BL_OK) return st;
   } else {
     // the columns first: dX may overwrite dY or X
     const int per = (a.M + parts - 1) / parts;
@@ -1806,7 +1870,18 @@ bl_status launch_norm_bwd(bl::NormGradArgs a, float* dweight, float* dbias, int 
     if ((st = last_cuda()) != BL_OK) return st;
     if (a.dX && (st = launch_norm_dx<LAYER, false>(a, stream)) != BL_OK) return st;
   }
-  bl::bl_norm_wgrad_join_kernel<<<a.K / 16, 1024, 0, stream>>>(a.part, parts, a.K, dweight, dbias, accumulate);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.part_cols / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, bl::bl_norm_wgrad_join_kernel, static_cast<const float*>(a.part), parts, a.part_cols,
+                         a.K, dweight, dbias, accumulate) != cudaSuccess)
+    return BL_ERR_CUDA;
   return last_cuda();
 }
 
@@ -1852,7 +1927,7 @@ bl_status bl_forward_checkpoint(const uint16_t* X, int norm, float eps, int64_t 
 
 size_t bl_backward_input_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (check_mnk(M, N, K) != BL_OK || M == 0) return 0;
-  const GradPlan g = plan_grad(bl::kGradInput, M, K, N);
+  const GradPlan g = plan_grad(bl::kGradInput, M, K, N, true);
   return g.pad_bytes + g.part_bytes;
 }
 
@@ -1883,9 +1958,8 @@ bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
 }
 
 size_t bl_backward_weight_workspace_bytes(int64_t M, int64_t K, int64_t N, unsigned flags) {
-  (void)flags;
   if (check_mnk(M, N, K) != BL_OK || M == 0) return 0;
-  const GradPlan g = plan_grad(bl::kGradWeight, M, K, N);
+  const GradPlan g = plan_grad(bl::kGradWeight, M, K, N, (flags & BL_GRAD_BF16) != 0);
   return g.pad_bytes + g.part_bytes;
 }
 

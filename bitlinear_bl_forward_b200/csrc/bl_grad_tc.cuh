@@ -59,7 +59,8 @@ template <int KIND, int TERMS, int BN>
 struct GtCfg {
   static constexpr int kBC = gt_bc(KIND, BN);
   static constexpr int kHalf = BN / 2;                         // r rows staged per CTA
-  static constexpr int kBBytes = kHalf * kBC * 2;              // K-major: boxes of 64 of the sum; MN-major: of 64 r
+  // K-major: boxes of 64 of the sum; MN-major: of 64 r (whole boxes)
+  static constexpr int kBBytes = (KIND == kGradInput ? kHalf : (kHalf + 63) / 64 * 64) * kBC * 2;
   static constexpr int kRawBytes = KIND == kGradInput ? kBC * kGtK / 4 : kBC * kGtK;
   static constexpr int kBlockBytes = kBC * 128;                // 64 k of an expanded tile
   static constexpr int kTileBytes = 2 * kBlockBytes;           // one expanded operand tile
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
               tma_load_2d(sB + j * C::kHalf * 128, &tmB, c * C::kBC + 64 * j, r0, &full[s]);
           } else {
 #pragma unroll
-            for (int j = 0; j < C::kHalf / 64; ++j)
+            for (int j = 0; j < (C::kHalf + 63) / 64; ++j)
               tma_load_2d(sB + j * C::kBlockBytes, &tmB, r0 + 64 * j, c * C::kBC, &full[s]);
           }
         }

@@ -18,10 +18,11 @@
 
 #include "bl_act.cuh"
 #include "bl_common.cuh"
+#include "bl_tc_common.cuh"
 
 namespace bl {
 
-constexpr int kNgMaxParts = 296;      // partial rows of the weight gradient (two CTAs an SM)
+constexpr int kNgSms = 148;           // CTAs of the weight gradient's partial rows: a multiple of the SMs
 constexpr int kNgRowMaxK = 8192;      // widest row whose weight gradient stays in registers
 
 __device__ __forceinline__ float2 warp_sum2(float2 v) {
@@ -60,6 +61,47 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ uint4 pack8_bf16(const float (&f)[8]) {
   return make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
+}
+
+// Pairs of fp32 (one instruction for both halves; each half rounds as usual).
+typedef uint64_t f2;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 f2_both(float v) { return f2_make(v, v); }
+__device__ __forceinline__ float2 f2_get(f2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 f2_bf16(uint32_t w) { return f2_make(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ void f2_bf16x8(uint4 v, f2 (&f)[4]) {
+  f[0] = f2_bf16(v.x);
+  f[1] = f2_bf16(v.y);
+  f[2] = f2_bf16(v.z);
+  f[3] = f2_bf16(v.w);
+}
+__device__ __forceinline__ uint32_t f2_pack_bf16(f2 a) {
+  uint32_t r;
+  asm("{\n\t.reg .f32 x, y;\n\tmov.b64 {x, y}, %1;\n\tcvt.rn.bf16x2.f32 %0, y, x;\n\t}" : "=r"(r) : "l"(a));
+  return r;
 }
 
 // 1 / sqrt(stat + eps): one rounding each.
@@ -134,17 +176,41 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// xh of 8 elements: from bf16 X, or from the 8-bit checkpoint (q / s).
-__device__ __forceinline__ void norm_xh_x(uint4 v, float mu, float r, float (&xh)[8]) {
-  unpack8_bf16(v, xh);
+// xh of 8 elements: from bf16 X, (x - mu) r, or from the 8-bit checkpoint, q / s.
+// (The difference first: folding -mu r into a product would lose what a large
+// mean cancels.)
+__device__ __forceinline__ void norm_xh_x(uint4 v, f2 neg_mu, f2 r, f2 (&xh)[4]) {
+  f2_bf16x8(v, xh);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) xh[e] = (xh[e] - mu) * r;
+  for (int e = 0; e < 4; ++e) xh[e] = f2_mul(f2_add(xh[e], neg_mu), r);
 }
-__device__ __forceinline__ void norm_xh_q(uint2 q, float inv_s, float (&xh)[8]) {
+__device__ __forceinline__ void norm_xh_q(uint2 q, f2 inv_s, f2 (&xh)[4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t w = e < 4 ? q.x : q.y;
-    xh[e] = static_cast<float>(static_cast<int>(w << (24 - 8 * (e & 3))) >> 24) * inv_s;
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = e < 2 ? q.x : q.y;
+    const int s = 16 * (e & 1);
+    const float lo = static_cast<float>(static_cast<int>(w << (24 - s)) >> 24);
+    const float hi = static_cast<float>(static_cast<int>(w << (16 - s)) >> 24);
+    xh[e] = f2_mul(f2_make(lo, hi), inv_s);
+  }
+}
+
+// dX of 8 elements from dY, the weight (all ones without one) and the row's
+// means c2 = mean(g xh), c1 = mean(g): (dY w - c1 - xh c2) r.
+__device__ __forceinline__ uint4 norm_dx8(const f2 (&dy)[4], const f2 (&w)[4], const f2 (&xh)[4], f2 neg_c1, f2 neg_c2,
+                                          f2 r) {
+  f2 d[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d[e] = f2_mul(f2_fma(xh[e], neg_c2, f2_fma(dy[e], w[e], neg_c1)), r);
+  return make_uint4(f2_pack_bf16(d[0]), f2_pack_bf16(d[1]), f2_pack_bf16(d[2]), f2_pack_bf16(d[3]));
+}
+
+__device__ __forceinline__ void norm_weight8(const uint16_t* weight, int i, f2 (&w)[4]) {
+  if (weight) {
+    f2_bf16x8(__ldg(reinterpret_cast<const uint4*>(weight) + i), w);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = f2_both(1.f);
   }
 }
 
@@ -157,113 +223,310 @@ struct NormGradArgs {
   const float* mean;       // [M] (LayerNorm on X)
   const float* stat;       // [M]
   uint16_t* dX;            // [M, K] or null; may be dY or X
-  float* part;             // [gridDim.x][2][K] partial dw and db, when GRADS
+  float* part;             // [parts][part_cols]: partial dw (if wanted), then db (if wanted)
   float eps;
   int M, K;
+  int want_w, want_b, part_cols;
 };
 
-// Row gradients; with GRADS also this CTA's part of dw and db.
-template <int C, bool LAYER, bool CKPT, bool GRADS>
-__global__ void __launch_bounds__(C >= 8 ? 1024 : 512) bl_norm_bwd_kernel(const NormGradArgs a) {
-  __shared__ float2 slots[2][32];
+// Sums of N values (a power of two, at most 32) over a group of nw warps,
+// returned to every thread.  Within a warp each halving step adds one half of
+// the values and hands the other half to the partner lane: N - 1 + 5 - log2 N
+// shuffles instead of 5 N.  One barrier (id `bar`, 32 nw threads); `slot`
+// ([32][N] floats) alternates between two buffers.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* slot, int w, int nw, int bar) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int m = N / 2; m >= 1; m >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float keep = up ? v[i + m] : v[i], send = up ? v[i] : v[i + m];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  float t = v[0];
+#pragma unroll
+  for (int p = 16 / N; p >= 1; p >>= 1) t += __shfl_xor_sync(0xffffffffu, t, p);
+  // lane l holds value l / (32 / N)
+  if ((lane & (32 / N - 1)) == 0) slot[w * N + lane / (32 / N)] = t;
+  named_bar_sync(bar, 32 * nw);
+  t = 0.f;
+  for (int i = lane / N; i < nw; i += 32 / N) t += slot[i * N + (lane & (N - 1))];
+#pragma unroll
+  for (int p = N; p < 32; p <<= 1) t += __shfl_xor_sync(0xffffffffu, t, p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t, i);
+}
+
+// Row gradients, one row a CTA.
+template <int C, bool LAYER, bool CKPT>
+__global__ void __launch_bounds__(512) bl_norm_dx_kernel(const NormGradArgs a) {
+  __shared__ float2 slot[32];
   const int nch = a.K >> 3;
   const float inv_k = 1.f / static_cast<float>(a.K);
-  float dw[GRADS ? 8 * C : 1], db[GRADS ? 8 * C : 1];
+  const int m = blockIdx.x;
+  const size_t base = static_cast<size_t>(m) * a.K;
+  uint4 vy[C], vx[CKPT ? 1 : C];
+  uint2 vq[CKPT ? C : 1];
 #pragma unroll
-  for (int e = 0; e < (GRADS ? 8 * C : 1); ++e) dw[e] = db[e] = 0.f;
-  int buf = 0;
-  for (int m = blockIdx.x; m < a.M; m += gridDim.x, buf ^= 1) {
-    const size_t base = static_cast<size_t>(m) * a.K;
-    const uint4* dyr = reinterpret_cast<const uint4*>(a.dY + base);
-    const uint4* xr = reinterpret_cast<const uint4*>(a.X + base);
-    const uint2* qr = reinterpret_cast<const uint2*>(a.Xq + base);
-    const float r = norm_rstd(a.stat[m], a.eps);
-    const float mu = (LAYER && !CKPT) ? a.mean[m] : 0.f;
-    const float inv_s = CKPT ? __fdiv_rn(1.f, a.scale[m]) : 0.f;
-    uint4 vy[C], vx[CKPT ? 1 : C];
-    uint2 vq[CKPT ? C : 1];
-    float2 s = make_float2(0.f, 0.f);
+  for (int j = 0; j < C; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    const bool in = i < nch;
+    vy[j] = in ? reinterpret_cast<const uint4*>(a.dY + base)[i] : make_uint4(0, 0, 0, 0);
+    if (CKPT)
+      vq[j] = in ? reinterpret_cast<const uint2*>(a.Xq + base)[i] : make_uint2(0, 0);
+    else
+      vx[j] = in ? reinterpret_cast<const uint4*>(a.X + base)[i] : make_uint4(0, 0, 0, 0);
+  }
+  const float r = norm_rstd(a.stat[m], a.eps);
+  const float mu = CKPT ? __fdiv_rn(1.f, a.scale[m]) : LAYER ? a.mean[m] : 0.f;   // CKPT: 1 / scale
+  const f2 f = f2_both(CKPT ? mu : r), nm = f2_both(-mu);
+  f2 sx = 0, sy = 0;   // bit pattern of (0, 0)
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int i = threadIdx.x + j * blockDim.x;
-      const bool in = i < nch;
-      vy[j] = in ? dyr[i] : make_uint4(0, 0, 0, 0);
+  for (int j = 0; j < C; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    if (i < nch) {
+      f2 dy[4], xh[4], w[4];
+      f2_bf16x8(vy[j], dy);
       if (CKPT)
-        vq[j] = in ? qr[i] : make_uint2(0, 0);
+        norm_xh_q(vq[CKPT ? j : 0], f, xh);
       else
-        vx[j] = in ? xr[i] : make_uint4(0, 0, 0, 0);
-    }
+        norm_xh_x(vx[CKPT ? 0 : j], nm, f, xh);
+      norm_weight8(a.weight, i, w);
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int i = threadIdx.x + j * blockDim.x;
-      if (i < nch) {
-        float g[8], xh[8];
-        unpack8_bf16(vy[j], g);
-        if (CKPT)
-          norm_xh_q(vq[j], inv_s, xh);
-        else
-          norm_xh_x(vx[j], mu, r, xh);
-        if (GRADS) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dw[8 * j + e] += g[e] * xh[e];
-            db[8 * j + e] += g[e];
-          }
-        }
-        if (a.weight) {
-          float w[8];
-          unpack8_bf16(__ldg(reinterpret_cast<const uint4*>(a.weight) + i), w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] *= w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s.x += g[e] * xh[e];
-          if (LAYER) s.y += g[e];
-        }
-      }
-    }
-    if (a.dX == nullptr) continue;   // the same for every thread
-    s = block_sum2(s, slots[buf]);
-    const float c2 = s.x * inv_k, c1 = LAYER ? s.y * inv_k : 0.f;
-    uint4* dxr = reinterpret_cast<uint4*>(a.dX + base);
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int i = threadIdx.x + j * blockDim.x;
-      if (i < nch) {
-        float g[8], xh[8];
-        unpack8_bf16(vy[j], g);
-        if (CKPT)
-          norm_xh_q(vq[j], inv_s, xh);
-        else
-          norm_xh_x(vx[j], mu, r, xh);
-        if (a.weight) {
-          float w[8];
-          unpack8_bf16(__ldg(reinterpret_cast<const uint4*>(a.weight) + i), w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] *= w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = (g[e] - xh[e] * c2 - c1) * r;
-        dxr[i] = pack8_bf16(g);
+      for (int e = 0; e < 4; ++e) {
+        const f2 g = f2_mul(dy[e], w[e]);
+        sx = f2_fma(g, xh[e], sx);
+        if (LAYER) sy = f2_add(g, sy);
       }
     }
   }
-  if (GRADS) {
-    float4* pw = reinterpret_cast<float4*>(a.part + static_cast<size_t>(blockIdx.x) * 2 * a.K);
-    float4* pb = pw + a.K / 4;
+  const float2 px = f2_get(sx), py = f2_get(sy);
+  const float2 s = block_sum2(make_float2(px.x + px.y, py.x + py.y), slot);
+  const f2 n2 = f2_both(-s.x * inv_k), n1 = f2_both(-s.y * inv_k), rr = f2_both(r);
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int i = threadIdx.x + j * blockDim.x;
-      if (i < nch) {
+  for (int j = 0; j < C; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    if (i < nch) {
+      f2 dy[4], xh[4], w[4];
+      f2_bf16x8(vy[j], dy);
+      if (CKPT)
+        norm_xh_q(vq[CKPT ? j : 0], f, xh);
+      else
+        norm_xh_x(vx[CKPT ? 0 : j], nm, f, xh);
+      norm_weight8(a.weight, i, w);
+      reinterpret_cast<uint4*>(a.dX + base)[i] = norm_dx8(dy, w, xh, n1, n2, rr);
+    }
+  }
+}
+
+// Row gradients and this CTA's part of dw and db, rows of up to 8192.
+//
+// Bound by reading dY and X and writing dX once.  A group of threads takes R
+// rows at a time; thread t owns the same columns of all of them, so that dw and
+// db stay in its registers.  Bulk copies keep the group's ring of ST stages in
+// shared memory filled, and both passes over a row (sums, then dX)
+// read it there, which leaves the registers to the column sums.  A CTA has G
+// groups, whose dw and db meet in shared memory: one partial row a CTA.
+
+template <int C, int R, int G, int ST, bool LAYER>
+__global__ void __launch_bounds__(G == 2 ? 640 : 512) bl_norm_bwd_kernel(const NormGradArgs a,
+                                                                          unsigned long long limit_ns) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  constexpr int NS = LAYER ? 2 * R : R;
+  __shared__ float slots[G][2][32 * NS];
+  __shared__ __align__(8) uint64_t full[G][ST];
+  const int T = blockDim.x / G, grp = G == 2 && threadIdx.x >= T ? 1 : 0, tid = threadIdx.x - grp * T;
+  const int nch = a.K >> 3, nw = T >> 5, w = tid >> 5;
+  const int step = gridDim.x * G * R;
+  const uint32_t row_bytes = 2 * a.K;
+  const float inv_k = 1.f / static_cast<float>(a.K);
+  uint8_t* my = ring + static_cast<size_t>(grp) * ST * R * 2 * row_bytes;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) mbar_init(&full[grp][i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  auto fetch = [&](int m0, int st) {   // one thread: rows m0.. of dY, then of X
+    const int n = min(R, a.M - m0);
+    if (n <= 0) return;
+    const uint32_t bytes = n * row_bytes;
+    uint8_t* d = my + static_cast<size_t>(st) * R * 2 * row_bytes;
+    mbar_arrive_expect_tx(&full[grp][st], 2 * bytes);
+    bulk_load(d, a.dY + static_cast<size_t>(m0) * a.K, bytes, &full[grp][st]);
+    bulk_load(d + R * row_bytes, a.X + static_cast<size_t>(m0) * a.K, bytes, &full[grp][st]);
+  };
+  f2 dw[4 * C], db[4 * C], wt[C][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int e = 8 * j + 4 * h;
-          pw[2 * i + h] = make_float4(dw[e], dw[e + 1], dw[e + 2], dw[e + 3]);
-          pb[2 * i + h] = make_float4(db[e], db[e + 1], db[e + 2], db[e + 3]);
+  for (int e = 0; e < 4 * C; ++e) dw[e] = db[e] = 0;   // bit pattern of (0, 0)
+#pragma unroll
+  for (int j = 0; j < C; ++j) norm_weight8(a.weight, min(tid + j * T, nch - 1), wt[j]);
+  int m0 = (blockIdx.x * G + grp) * R;
+  if (tid == 0)
+    for (int i = 0; i < ST && m0 + i * step < a.M; ++i) fetch(m0 + i * step, i);
+  // the rows' statistics, one step ahead
+  float stat[R], mean[R];
+  auto stats = [&](int m) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const bool row = m + q < a.M;
+      stat[q] = row ? a.stat[m + q] : 1.f;
+      mean[q] = LAYER && row ? a.mean[m + q] : 0.f;
+    }
+  };
+  stats(m0);
+  for (int it = 0, st = 0, ph = 0; m0 < a.M; m0 += step, ++it) {
+    f2 r[R], nm[R];
+    float s[NS];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      r[q] = f2_both(norm_rstd(stat[q], a.eps));
+      nm[q] = f2_both(-mean[q]);
+    }
+    if (m0 < a.M - step) stats(m0 + step);
+    // a wait that gives up is recorded in the status word; the rows are then
+    // whatever the stage holds
+    mbar_wait(&full[grp][st], ph, nullptr, limit_ns, kSiteNormRows);
+    const uint8_t* rows = my + static_cast<size_t>(st) * R * 2 * row_bytes;
+    auto load = [&](int q, int i, f2 (&dy)[4], f2 (&xh)[4]) {
+      f2_bf16x8(*reinterpret_cast<const uint4*>(rows + q * row_bytes + 16 * i), dy);
+      norm_xh_x(*reinterpret_cast<const uint4*>(rows + (R + q) * row_bytes + 16 * i), nm[q], r[q], xh);
+    };
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      f2 sx = 0, sy = 0;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int i = tid + j * T;
+        if (i < nch && m0 + q < a.M) {
+          f2 dy[4], xh[4];
+          load(q, i, dy, xh);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const f2 p = f2_mul(dy[e], xh[e]);
+            dw[4 * j + e] = f2_add(dw[4 * j + e], p);
+            db[4 * j + e] = f2_add(db[4 * j + e], dy[e]);
+            sx = f2_fma(p, wt[j][e], sx);
+            if (LAYER) sy = f2_fma(dy[e], wt[j][e], sy);
+          }
+        }
+      }
+      const float2 x = f2_get(sx), y = f2_get(sy);
+      s[q] = x.x + x.y;
+      if (LAYER) s[(LAYER ? R : 0) + q] = y.x + y.y;
+    }
+    // the barrier inside also says that the group has left the stage before
+    if (a.dX)
+      group_sum<NS>(s, slots[grp][it & 1], w, nw, 1 + grp);
+    else
+      named_bar_sync(1 + grp, T);
+    if (it > 0 && tid == 0 && m0 < a.M - (ST - 1) * step) fetch(m0 + (ST - 1) * step, st == 0 ? ST - 1 : st - 1);
+    if (++st == ST) {
+      st = 0;
+      ph ^= 1;
+    }
+    if (!a.dX) continue;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      if (m0 + q >= a.M) continue;
+      const f2 n2 = f2_both(-s[q] * inv_k), n1 = f2_both(LAYER ? -s[(LAYER ? R : 0) + q] * inv_k : 0.f);
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int i = tid + j * T;
+        if (i < nch) {
+          f2 dy[4], xh[4];
+          load(q, i, dy, xh);
+          reinterpret_cast<uint4*>(a.dX + static_cast<size_t>(m0 + q) * a.K)[i] =
+              norm_dx8(dy, wt[j], xh, n1, n2, r[q]);
         }
       }
     }
+  }
+  pdl_launch_dependents();
+  if (G == 2) {
+    ulonglong2* merge = reinterpret_cast<ulonglong2*>(ring);   // [2][K] floats
+    __syncthreads();                                   // both groups have left the ring
+    if (grp == 1) {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = tid + j * T, e = 4 * j + 2 * h;
+          if (i < nch) {
+            merge[2 * i + h] = make_ulonglong2(dw[e], dw[e + 1]);
+            merge[2 * (nch + i) + h] = make_ulonglong2(db[e], db[e + 1]);
+          }
+        }
+    }
+    __syncthreads();
+    if (grp == 1) return;
+  }
+  const ulonglong2* merge = reinterpret_cast<const ulonglong2*>(ring);
+  ulonglong2* pw = reinterpret_cast<ulonglong2*>(a.part + static_cast<size_t>(blockIdx.x) * a.part_cols);
+  ulonglong2* pb = pw + (a.want_w ? a.K / 4 : 0);
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int i = tid + j * T;
+    if (i >= nch) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = 4 * j + 2 * h;
+      ulonglong2 u = make_ulonglong2(dw[e], dw[e + 1]), v = make_ulonglong2(db[e], db[e + 1]);
+      if (G == 2) {
+        const ulonglong2 u2 = merge[2 * i + h], v2 = merge[2 * (nch + i) + h];
+        u = make_ulonglong2(f2_add(u.x, u2.x), f2_add(u.y, u2.y));
+        v = make_ulonglong2(f2_add(v.x, v2.x), f2_add(v.y, v2.y));
+      }
+      if (a.want_w) pw[2 * i + h] = u;
+      if (a.want_b) pb[2 * i + h] = v;
+    }
+  }
+}
+
+// Row gradients of wide rows, which do not fit the registers: the sums in one
+// pass over the row, dX in a second one (the row is in L2 by then).  A thread
+// reads again only what it will overwrite itself, so dX may be dY or X.
+template <bool LAYER, bool CKPT>
+__global__ void __launch_bounds__(1024) bl_norm_dx_wide_kernel(const NormGradArgs a) {
+  __shared__ float2 slot[32];
+  const int nch = a.K >> 3;
+  const int m = blockIdx.x;
+  const size_t base = static_cast<size_t>(m) * a.K;
+  const float r = norm_rstd(a.stat[m], a.eps);
+  const float mu = CKPT ? __fdiv_rn(1.f, a.scale[m]) : LAYER ? a.mean[m] : 0.f;
+  const f2 f = f2_both(CKPT ? mu : r), nm = f2_both(-mu);
+  auto load = [&](int i, f2 (&dy)[4], f2 (&xh)[4], f2 (&w)[4]) {
+    f2_bf16x8(reinterpret_cast<const uint4*>(a.dY + base)[i], dy);
+    if (CKPT)
+      norm_xh_q(reinterpret_cast<const uint2*>(a.Xq + base)[i], f, xh);
+    else
+      norm_xh_x(reinterpret_cast<const uint4*>(a.X + base)[i], nm, f, xh);
+    norm_weight8(a.weight, i, w);
+  };
+  f2 sx = 0, sy = 0;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < nch; i += blockDim.x) {
+    f2 dy[4], xh[4], w[4];
+    load(i, dy, xh, w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f2 g = f2_mul(dy[e], w[e]);
+      sx = f2_fma(g, xh[e], sx);
+      if (LAYER) sy = f2_add(g, sy);
+    }
+  }
+  const float2 px = f2_get(sx), py = f2_get(sy);
+  const float2 s = block_sum2(make_float2(px.x + px.y, py.x + py.y), slot);
+  const float inv_k = 1.f / static_cast<float>(a.K);
+  const f2 n2 = f2_both(-s.x * inv_k), n1 = f2_both(-s.y * inv_k), rr = f2_both(r);
+#pragma unroll 2
+  for (int i = threadIdx.x; i < nch; i += blockDim.x) {
+    f2 dy[4], xh[4], w[4];
+    load(i, dy, xh, w);
+    reinterpret_cast<uint4*>(a.dX + base)[i] = norm_dx8(dy, w, xh, n1, n2, rr);
   }
 }
 
@@ -272,44 +535,45 @@ template <bool LAYER>
 __global__ void __launch_bounds__(128) bl_norm_wgrad_cols_kernel(const NormGradArgs a, int rows_per_part) {
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= (a.K >> 3)) return;
-  float dw[8], db[8];
+  f2 dw[4], db[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dw[e] = db[e] = 0.f;
+  for (int e = 0; e < 4; ++e) dw[e] = db[e] = 0;
   const int m0 = blockIdx.y * rows_per_part, m1 = min(a.M, m0 + rows_per_part);
 #pragma unroll 4
   for (int m = m0; m < m1; ++m) {
     const size_t base = static_cast<size_t>(m) * a.K;
-    const float r = norm_rstd(a.stat[m], a.eps);
-    const float mu = LAYER ? a.mean[m] : 0.f;
-    float g[8], xh[8];
-    unpack8_bf16(reinterpret_cast<const uint4*>(a.dY + base)[i], g);
-    norm_xh_x(reinterpret_cast<const uint4*>(a.X + base)[i], mu, r, xh);
+    const f2 r = f2_both(norm_rstd(a.stat[m], a.eps)), nm = f2_both(LAYER ? -a.mean[m] : 0.f);
+    f2 dy[4], xh[4];
+    f2_bf16x8(reinterpret_cast<const uint4*>(a.dY + base)[i], dy);
+    norm_xh_x(reinterpret_cast<const uint4*>(a.X + base)[i], nm, r, xh);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dw[e] += g[e] * xh[e];
-      db[e] += g[e];
+    for (int e = 0; e < 4; ++e) {
+      dw[e] = f2_fma(dy[e], xh[e], dw[e]);
+      db[e] = f2_add(dy[e], db[e]);
     }
   }
-  float4* pw = reinterpret_cast<float4*>(a.part + static_cast<size_t>(blockIdx.y) * 2 * a.K);
-  float4* pb = pw + a.K / 4;
+  ulonglong2* pw = reinterpret_cast<ulonglong2*>(a.part + static_cast<size_t>(blockIdx.y) * a.part_cols);
+  ulonglong2* pb = pw + (a.want_w ? a.K / 4 : 0);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    pw[2 * i + h] = make_float4(dw[4 * h], dw[4 * h + 1], dw[4 * h + 2], dw[4 * h + 3]);
-    pb[2 * i + h] = make_float4(db[4 * h], db[4 * h + 1], db[4 * h + 2], db[4 * h + 3]);
+    if (a.want_w) pw[2 * i + h] = make_ulonglong2(dw[2 * h], dw[2 * h + 1]);
+    if (a.want_b) pb[2 * i + h] = make_ulonglong2(db[2 * h], db[2 * h + 1]);
   }
 }
 
 // Sums the parts in a fixed order: 32 columns a CTA, 32 threads a column.
-// Columns 0..K-1 are dw, K..2K-1 db.
+// Launched to start while the kernel before it still runs: it waits for that
+// kernel's memory before it reads.
 __global__ void __launch_bounds__(1024)
-    bl_norm_wgrad_join_kernel(const float* __restrict__ part, int parts, int K, float* __restrict__ dweight,
+    bl_norm_wgrad_join_kernel(const float* __restrict__ part, int parts, int cols, int K, float* __restrict__ dweight,
                               float* __restrict__ dbias, int accumulate) {
   __shared__ float t[32][33];
   const int cx = threadIdx.x & 31, py = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cx;   // 2K is a multiple of 32
+  const float* p = part + blockIdx.x * 32 + cx;   // cols is a multiple of 32
+  pdl_wait();
   float s = 0.f;
-#pragma unroll 4
-  for (int p = py; p < parts; p += 32) s += part[static_cast<size_t>(p) * 2 * K + c];
+#pragma unroll 8
+  for (int i = py; i < parts; i += 32) s += p[static_cast<size_t>(i) * cols];
   t[py][cx] = s;
   __syncthreads();
   s = t[cx][py];   // column py of the block, part group cx
@@ -317,9 +581,9 @@ __global__ void __launch_bounds__(1024)
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (cx == 0) {
     const int col = blockIdx.x * 32 + py;
-    float* out = col < K ? dweight : dbias;
-    const int k = col < K ? col : col - K;
-    if (out) out[k] = accumulate ? out[k] + s : s;
+    const bool w = dweight && col < K;
+    float* out = w ? dweight + col : dbias + (dweight ? col - K : col);
+    *out = accumulate ? *out + s : s;
   }
 }
 
