@@ -1832,7 +1832,7 @@ inline int norm_parts(int64_t M, int64_t K) {
     const NormShape n = norm_shape(K);
     const int smem = n.g * n.st * n.r * 2 * static_cast<int>(K) * 2 + 2048;
     const int threads = n.g * row_threads(static_cast<int>(K), n.c);
-    const int occ = std::max(1, std::min(220 * 1024 / smem, 1280 / threads));
+    const int occ = std::max(1, std::min(2, std::min(220 * 1024 / smem, 1280 / threads)));
     return static_cast<int>(std::min<int64_t>((M + n.r * n.g - 1) / (n.r * n.g), occ * bl::kNgSms));
   }
   const int64_t want = std::max<int64_t>(1, (int64_t(1184) * 1024) / K);
