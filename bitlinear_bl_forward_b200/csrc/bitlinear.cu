@@ -620,10 +620,10 @@ bl_status launch_tc2_t(const int8_t* Xq, int M, int K, int N, const uint8_t* Wp,
 }
 
 // Largest number of two-CTA clusters of `kernel` that are resident at once on
-// the current device (cached per device).
+// the current device (cached per device in the kernel's own `cache`: kernels
+// may share a type).
 template <typename F>
-int max_active_pairs(F* kernel, int threads, int smem) {
-  static std::atomic<int> cache[kMaxDevices];
+int max_active_pairs(F* kernel, int threads, int smem, std::atomic<int>* cache) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   int v = cache[dev].load(std::memory_order_relaxed);
@@ -699,7 +699,8 @@ bl_status launch_tc_pair_multi(const int8_t* Xq, int M, int K, const TcProb* pro
   cudaLaunchConfig_t cfg = {};
   // a persistent grid must fit in one wave: not every SM can host half of a
   // two-SM cluster, so ask how many clusters are co-resident (once per device)
-  int npairs = max_active_pairs(bl::bl_mma_pair_kernel, bl::kQThreads, bl::kQSmemBytes);
+  static std::atomic<int> pairs[kMaxDevices];
+  int npairs = max_active_pairs(bl::bl_mma_pair_kernel, bl::kQThreads, bl::kQSmemBytes, pairs);
   if (npairs <= 0) return BL_ERR_CUDA;
   if (npairs > ntiles) npairs = ntiles;
   cfg.gridDim = dim3(2 * npairs);
@@ -1596,11 +1597,13 @@ bl_status check_rows(int64_t M, int64_t K) {
   return check_m(M, K);
 }
 
-// N*K, M*K and M*N below 2^40.
+// N*K, M*K and M*N below 2^40; M and N leave 32-bit tile and row counters room
+// to step past the end.
 bl_status check_mnk(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kMaxDim = int64_t(INT32_MAX) - 65536;
   bl_status st = check_shape_nk(N, K);
   if (st != BL_OK) return st;
-  if (N > INT32_MAX) return BL_ERR_SHAPE;
+  if (N > kMaxDim || M > kMaxDim) return BL_ERR_SHAPE;
   if ((st = check_m(M, K)) != BL_OK) return st;
   if (M > 0 && M >= kMaxElems / N) return BL_ERR_SHAPE;
   return BL_OK;
@@ -1619,34 +1622,42 @@ struct GradPlan {
 constexpr int kGradPlanPairs = 74;   // CTA pairs of a B200
 
 // Tiles of 256 k by bn r on 74 CTA pairs, and the number of parts of the sum:
-// whichever takes least by this model of the kernel (us, measured at full
-// waves): a stage costs (bn + f) / (256 + f) of its time at bn = 256 (tensor
-// work plus what a stage costs anyway: f = 48, or 128 with the weight gradient's
-// conversions), pairs work in waves of whole items, and parts are written and
-// read once more and need a second launch.  What it decides,
-// measured: 4096 x 2560 of a 2B layer's input gradient at bn = 192 (three waves
-// of 220 tiles, 101 us) instead of 256 (three of 160, 132 us); its weight
-// gradient at 256 (four waves, 193 us) instead of 192 (five, 199 us).
+// whichever takes least by this model of the kernel, in us.
+//   * 64 rows of the sum take `stage`, about the same for every bn up to 128
+//     (there the expanded operand's way through shared memory is the limit);
+//   * pairs work in waves of whole items; a wave is as long as its sums, or as
+//     its epilogues where those are longer (few rows);
+//   * parts are written and read once more, and need a second launch.
+// Both sides measured: the 2B down projection's input gradient at bn = 256
+// takes 93 us, at 192 more; the up projection's (4096 x 2560 out) takes 105 us at
+// 192 (three waves) where 256 needs three of its longer ones; 300 tokens take
+// 20 us at 128 in two parts, 26 in one, 38 at 256.
 GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N, bool bf16_out) {
+  struct Shape {
+    int bn;
+    double stage, epilogue;
+  };
+  static const Shape input[5] = {{256, 0.36, 2.0}, {192, 0.325, 1.6}, {128, 0.22, 1.2}, {64, 0.21, 0.8}, {32, 0.21, 0.6}};
+  static const Shape weight32[3] = {{256, 0.74, 4.0}, {192, 0.63, 3.2}, {128, 0.49, 2.2}};
+  static const Shape weight16[3] = {{256, 0.45, 2.8}, {192, 0.43, 2.4}, {128, 0.40, 1.6}};
   GradPlan g = {};
   const int64_t R = kind == bl::kGradInput ? M : N, L = kind == bl::kGradInput ? N : M;
   const int64_t kt = (K + 2 * bl::kGtK - 1) / (2 * bl::kGtK);
-  const double t256 = kind == bl::kGradInput ? 0.38 : bf16_out ? 0.45 : 0.75;   // 64 rows of the sum
-  const double fixed = kind == bl::kGradInput ? 48 : 128;
-  const int bns[5] = {256, 192, 128, 64, 32};
+  const Shape* shapes = kind == bl::kGradInput ? input : bf16_out ? weight16 : weight32;
   double best = 1e300;
   for (int b = 0; b < (kind == bl::kGradInput ? 5 : 3); ++b) {
-    const int bn = bns[b], bc = bl::gt_bc(kind, bn);
+    const int bn = shapes[b].bn, bc = bl::gt_bc(kind, bn);
     const int64_t rt = (R + bn - 1) / bn, tiles = kt * rt, nk = (L + bc - 1) / bc;
-    const double stage = t256 * (bn + fixed) / (256 + fixed) * (bc / 64);
+    const double stage = shapes[b].stage * (bc / 64);
     const int64_t fill = std::max<int64_t>(1, kGradPlanPairs / tiles);
     const int64_t tries[6] = {1, 2, 3, 4, fill, 2 * fill};
     for (int j = 0; j < (tiles > 4 * kGradPlanPairs ? 1 : 6); ++j) {
       const int64_t want = std::min<int64_t>(tries[j], std::max<int64_t>(1, nk / 2));
       const int64_t per = (nk + want - 1) / want, splits = (nk + per - 1) / per;
       const int64_t waves = (tiles * splits + kGradPlanPairs - 1) / kGradPlanPairs;
-      double t = static_cast<double>(waves) * (static_cast<double>(per) * stage + 0.5);
-      if (splits > 1) t += 2.5 + static_cast<double>(splits) * R * K * 8 / 5e6;
+      double t = static_cast<double>(waves) * std::max(static_cast<double>(per) * stage, shapes[b].epilogue) +
+                 shapes[b].epilogue;
+      if (splits > 1) t += 2.5 + static_cast<double>(splits) * R * K * 8 / 8e6;
       if (t < best) {
         best = t;
         g.bn = bn;
@@ -1710,14 +1721,25 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
       encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, M, N, static_cast<uint64_t>(g.ld) * 2,
                 KIND == bl::kGradInput ? C::kHalf : C::kBC, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return BL_ERR_CUDA;
-  if (P.mode == bl::kGtTmaBf16) {
-    if (!encode_2d(&tmD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, static_cast<uint64_t>(P.R), K, K * 2, C::kChunk, 32,
-                   CU_TENSOR_MAP_SWIZZLE_NONE))
-      return BL_ERR_CUDA;
-  } else {
+  // output tiles: [parts][R][K] (a tile that ends past R is clipped there)
+  if (P.mode == bl::kGtBf16Acc) {
     tmD = tmB;   // not used
+  } else {
+    EncodeTiledFn enc = get_encode();
+    const bool bf16 = P.mode == bl::kGtTmaBf16;
+    const cuuint64_t rs = K * (bf16 ? 2 : 4);
+    const cuuint64_t dims[3] = {K, static_cast<cuuint64_t>(P.R), static_cast<cuuint64_t>(g.splits)};
+    const cuuint64_t strides[2] = {rs, g.splits > 1 ? rs * static_cast<cuuint64_t>(P.R) : rs};
+    const cuuint32_t box[3] = {32, bf16 ? static_cast<cuuint32_t>(C::kChunk) : 16, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (!enc ||
+        enc(&tmD, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, P.out, dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return BL_ERR_CUDA;
   }
-  int npairs = max_active_pairs(kern, C::kThreads, C::kSmemBytes);
+  static std::atomic<int> pairs[kMaxDevices];
+  int npairs = max_active_pairs(kern, C::kThreads, C::kSmemBytes, pairs);
   if (npairs <= 0) return BL_ERR_CUDA;
   const int64_t items = static_cast<int64_t>(g.kt) * g.rt * g.splits;
   if (npairs > items) npairs = static_cast<int>(items);

@@ -77,7 +77,7 @@ struct GtCfg {
   static constexpr int kFirstEpi = 2 + kGroupWarps * kGroups;
   static constexpr int kThreads = 32 * (kFirstEpi + kGtEpiWarps);
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;       // r of one epilogue step
-  static constexpr int kOutBytes = TERMS == 1 ? kChunk * 64 : 0;   // bf16 staging tile [r][32 k] a warp
+  static constexpr int kOutBytes = TERMS == 2 ? 4096 : 2048;   // staging a warp: tiles of [32 r][32 k] bf16 or [16 r][32 k] fp32
   static constexpr int kOutTotal = kGtEpiWarps * kOutBytes;
   static constexpr int kASlots = kBC == 128 || TERMS == 2 ? 3 : 4;   // being expanded, and one being read
   static constexpr int kBudget = 227 * 1024 - 1024 - 512 - kOutTotal - kASlots * kASlotBytes;
@@ -198,11 +198,23 @@ __device__ __forceinline__ void gt_arrive_leader(uint64_t* bar) {
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-// Add to global memory without reading it back (rounds to nearest).  Every
-// output element has one thread that adds to it, in order, so the result does
-// not depend on the run.
-__device__ __forceinline__ void red_add_f32(float* p, float v) {
-  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+// TMA store of a tile, and the reduction that adds it to fp32 in memory
+// (rounding to nearest).  Every output element has one thread that adds to it, in
+// order, so the result does not depend on the run.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tmap, int x, int y, int z, const void* smem_src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
+               : "memory");
+}
+__device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* tmap, int x, int y, int z, const void* smem_src) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_wait_group_read1() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
@@ -381,7 +393,10 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         item(it, kt, rt, c0, c1, part);
         while (c0 < c1) {   // a segment: the accumulator that was drained longest ago
           const int b = i & 1, ce = min(c1, c0 + min(C::kSegment, c1 - c0));
-          if (i >= 2 && !mbar_wait(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc)) {
+          // (every decision to give up is taken by the whole warp: elect.sync
+          // below names all its lanes)
+          if (i >= 2 &&
+              !__all_sync(0xffffffffu, mbar_wait(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc))) {
             stop = true;
             break;
           }
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           const uint32_t d_tmem = tmem + b * BN;
           uint32_t acc = 0;
           for (; c0 < ce; ++c0) {
-            if (!__all_sync(0xffffffffu, seen) && !mbar_wait(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull)) {
+            if (!__all_sync(0xffffffffu, seen || mbar_wait(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull))) {
               stop = true;
               break;
             }
@@ -514,24 +529,39 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     }
   } else {
     // ---------------- epilogue (both CTAs) ----------------
+    // A warp has 32 k (its lanes) of half of the tile's r.  Results leave through
+    // staging tiles and TMA: stores, or reductions that add
+    // to fp32 in memory (plain stores of 128 bytes a warp took 7100 clocks a tile,
+    // the adds 8600).  A bf16 result that is added to is read and rounded once.
     const int q = warp & 3, half = (warp - C::kFirstEpi) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float f = P.gamma ? *P.gamma : 1.f;
     uint8_t* so = sOut + (warp - C::kFirstEpi) * C::kOutBytes;
-    int i = 0;
+    int i = 0, buf = 0;
     int kt = 0, rt = 0, c0 = 0, c1 = 0, part = 0;
     for (int it = pair; it < nitems; ++i) {
       if (c0 >= c1) item(it, kt, rt, c0, c1, part);
-      // the segments after the first add to what this thread stored itself
-      const int mode = P.mode == kGtF32 && c0 != part * P.per ? kGtF32Acc : P.mode;
       const int b = i & 1;
+      const int kw = kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32, k = kw + lane;
+      const int r0 = rt * BN + half * C::kHalf;
+      const bool kin = kw < P.K;   // K is a multiple of 64: a warp's 32 k are all inside or all outside
+      if (P.mode == kGtBf16Acc && kin) {
+        // what will be added to, into L2 while the sum is formed
+        for (int t = lane; t < C::kHalf && r0 + t < P.R; t += 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t*>(P.out) +
+                                                        static_cast<size_t>(r0 + t) * P.K + kw));
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (i >> 1) & 1, abort_flag, limit_ns, kSiteAcc) &&
                                        !*abort_flag))
         break;
       tc_fence_after();
-      const int kw = kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32, k = kw + lane;
-      const int r0 = rt * BN + half * C::kHalf;
-      const bool kin = kw < P.K;   // K is a multiple of 64: a warp's 32 k are all inside or all outside
+      // the segments after the first add to what this warp stored itself: those
+      // stores have to be complete
+      const bool add = P.mode == kGtF32Acc || (P.mode == kGtF32 && c0 != part * P.per);
+      if (add) {
+        if (lane == 0) bulk_wait_group0();
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int c = 0; c < C::kHalf; c += C::kChunk) {
         uint32_t v[32];
@@ -542,45 +572,58 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         tmem_wait_ld();
         const int r = r0 + c;
         if (!kin || r >= P.R) continue;
-        if (mode == kGtTmaBf16) {
-          uint8_t* tile = so;
-          if (lane == 0) bulk_wait_group_read0();   // the last store has read the tile
-          __syncwarp();
+        if (P.mode != kGtBf16Acc) {
+          if (P.mode == kGtTmaBf16) {
+            if (lane == 0) bulk_wait_group_read0();   // the last store has read the tile
+            __syncwarp();
 #pragma unroll
-          for (int t = 0; t < C::kChunk; ++t)
-            reinterpret_cast<uint16_t*>(tile)[t * 32 + lane] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[t]) * f));
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tmD, kw, r, tile);
-            bulk_commit_group();
+            for (int t = 0; t < C::kChunk; ++t)
+              reinterpret_cast<uint16_t*>(so)[t * 32 + lane] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[t]) * f));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&tmD, kw, r, part, so);
+              bulk_commit_group();
+            }
+            continue;
+          }
+#pragma unroll
+          for (int h = 0; h < C::kChunk; h += 16) {
+            if (r + h >= P.R) break;
+            uint8_t* tile = so + (TERMS == 2 ? buf * 2048 : 0);   // two tiles in turn, or one
+            buf ^= 1;
+            if (lane == 0) {
+              if (TERMS == 2)
+                bulk_wait_group_read1();
+              else
+                bulk_wait_group_read0();
+            }
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < 16; ++t) reinterpret_cast<uint32_t*>(tile)[t * 32 + lane] = v[h + t];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (add)
+                tma_reduce_add_3d(&tmD, kw, r + h, part, tile);
+              else
+                tma_store_3d(&tmD, kw, r + h, part, tile);
+              bulk_commit_group();
+            }
           }
         } else {
-          const size_t o = (static_cast<size_t>(part) * P.R + r) * P.K + k;
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.out) + static_cast<size_t>(r) * P.K + k;
           const int n = min(C::kChunk, P.R - r);
           const uint32_t ld = static_cast<uint32_t>(P.K);
-          if (mode == kGtF32) {
-            float* y = static_cast<float*>(P.out) + o;
 #pragma unroll
-            for (int t = 0; t < C::kChunk; ++t)
-              if (t < n) y[t * ld] = __uint_as_float(v[t]);
-          } else if (mode == kGtF32Acc) {
-            float* y = static_cast<float*>(P.out) + o;
+          for (int h = 0; h < C::kChunk; h += 16) {
+            float old[16];
 #pragma unroll
-            for (int t = 0; t < C::kChunk; ++t)
-              if (t < n) red_add_f32(y + t * ld, __uint_as_float(v[t]));
-          } else {
-            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.out) + o;
+            for (int t = 0; t < 16; ++t) old[t] = h + t < n ? __bfloat162float(y[(h + t) * ld]) : 0.f;
 #pragma unroll
-            for (int h = 0; h < C::kChunk; h += 16) {
-              float old[16];
-#pragma unroll
-              for (int t = 0; t < 16; ++t) old[t] = h + t < n ? __bfloat162float(y[(h + t) * ld]) : 0.f;
-#pragma unroll
-              for (int t = 0; t < 16; ++t)
-                if (h + t < n) y[(h + t) * ld] = __float2bfloat16_rn(old[t] + __uint_as_float(v[h + t]));
-            }
+            for (int t = 0; t < 16; ++t)
+              if (h + t < n) y[(h + t) * ld] = __float2bfloat16_rn(old[t] + __uint_as_float(v[h + t]));
           }
         }
       }

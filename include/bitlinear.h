@@ -449,8 +449,10 @@ BL_API bl_status bl_forward_checkpoint(const uint16_t* X, int norm, float eps, i
  * Gradient of the (normalised) input:
  *   dX[m,k] = bf16_rn( gamma * sum_n dY[m,n] * C[n,k] )     fp32 sums
  * dY: bf16 bits [M, N], 16-byte aligned.  Wp, gamma as in bl_forward.  dX:
- * bf16 bits [M, K], 16-byte aligned.  Any N; M == 0 is a no-op.  Results do
- * not depend on the run (no atomics).  workspace:
+ * bf16 bits [M, K], 16-byte aligned, not overlapping dY.  Any N (a row of dY that
+ * is not a multiple of 16 bytes costs a padded copy in the workspace); M and N
+ * below 2^31 - 65536, M*N below 2^40, else BL_ERR_SHAPE.  M == 0 is a no-op.
+ * Results do not depend on the run.  workspace:
  * bl_backward_input_workspace_bytes(M, K, N) bytes (may be 0), 16-byte aligned.
  */
 BL_API size_t bl_backward_input_workspace_bytes(int64_t M, int64_t K, int64_t N);
@@ -469,8 +471,8 @@ BL_API bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int
  * product at most), a bf16 dW as one bf16 (2^-8, like its own rounding): half
  * the tensor-core work.
  * dY: bf16 bits [M, N], 16-byte aligned.  Xq: int8 [M, K], 16-byte aligned.
- * scale: fp32 [M], positive, 4-byte aligned.  dW: 16-byte aligned.  Any N.
- * M == 0 writes zeros (nothing with BL_GRAD_ACCUMULATE).  Results do not
+ * scale: fp32 [M], positive normal numbers, 4-byte aligned.  dW: 16-byte
+ * aligned.  N and limits as in bl_backward_input.  M == 0 writes zeros (nothing with BL_GRAD_ACCUMULATE).  Results do not
  * depend on the run.  workspace: bl_backward_weight_workspace_bytes(M, K, N,
  * flags) bytes (may be 0), 16-byte aligned.
  */
