@@ -496,3 +496,114 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         bl.bl_norm_backward(X, X, bl.BL_NORM_RMS, s, weight=torch.ones(K, dtype=torch.bfloat16, device="cuda"),
                             accumulate=True)
+
+
+# One shape for every tile width (32..256 rows of the output) with the sum whole
+# and split, as the cost model chooses them.
+REACH_INPUT = [(33, 64, 1003), (2500, 64, 33), (390, 64, 1500), (2500, 320, 33), (1000, 64, 2050), (1030, 2112, 33),
+               (130, 4160, 4100), (4100, 4160, 33), (4100, 64, 4100)]
+REACH_WEIGHT = [(640, 64, 33), (33, 4160, 520), (2049, 64, 4100), (520, 1088, 3001), (2500, 64, 4100), (770, 64, 33),
+                (4100, 1344, 130), (33, 4160, 3001), (1500, 64, 4100)]
+
+
+@pytest.mark.parametrize("M,K,N", REACH_INPUT)
+def test_backward_input_tiles(M, K, N):
+    _, Wp, gamma, C, _, _ = layer(M, K, N, 1)
+    dY = grads(M, N, 2)
+    dX = Guarded((M, K), torch.bfloat16)
+    ws = Guarded((max(16, bl.bl_backward_input_workspace_bytes(M, K, N)),), torch.uint8)
+    bl.bl_backward_input(dY, Wp, gamma, K, out=dX.t, workspace=ws.t)
+    assert dX.intact() and ws.intact()
+    check_dx(dX.t, dY, C, gamma)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K,N", REACH_WEIGHT)
+def test_backward_weight_tiles(M, K, N, dtype):
+    *_, q, s = layer(M, K, N, 1)
+    dY = grads(M, N, 2)
+    flags = bl.BL_GRAD_BF16 if dtype == torch.bfloat16 else 0
+    for acc in (False, True):
+        dW = Guarded((N, K), dtype)
+        base = None
+        if acc:
+            base = (torch.randn(N, K, generator=torch.Generator().manual_seed(3)) * 1e-2).to(dtype).cuda()
+            dW.t.copy_(base)
+        ws = Guarded((max(16, bl.bl_backward_weight_workspace_bytes(M, K, N, flags | acc)),), torch.uint8)
+        bl.bl_backward_weight(dY, q, s, out=dW.t, accumulate=acc, workspace=ws.t)
+        assert dW.intact() and ws.intact()
+        check_dw(dW.t, dY, q, s, base=base)
+
+
+def test_positive_products_over_many_tokens():
+    # sums that only grow show what the accumulator truncates
+    M, K, N = 16384, 64, 136
+    q = torch.randint(1, 128, (M, K), generator=torch.Generator().manual_seed(1)).to(torch.int8).cuda()
+    s = (torch.rand(M, generator=torch.Generator().manual_seed(2)) + 0.5).cuda()
+    dY = grads(M, N, 3).abs()
+    want = dY.to(F64).t() @ (q.to(F64) / s.to(F64)[:, None])
+    got = bl.bl_backward_weight(dY, q, s)
+    check_dw(got, dY, q, s)
+    assert ((got.to(F64) - want).norm() / want.norm()).item() <= 2.0**-16
+
+
+def test_norm_backward_captured_and_concurrent():
+    """The backward with weight gradients in a graph, replayed on new contents;
+    and two different calls at once on two streams with their own workspaces."""
+    M, K = 300, 2560
+    w = torch.randn(K).to(torch.bfloat16).cuda()
+    X, dY = torch.randn(M, K).to(torch.bfloat16).cuda(), grads(M, K, 1)
+
+    def both(x, dy):
+        Y, mean, stat = bl.bl_norm_forward(x, bl.BL_NORM_LAYER, weight=w)
+        return (Y, *bl.bl_norm_backward(dy, x, bl.BL_NORM_LAYER, stat, mean=mean, weight=w, need_bias=True))
+
+    both(X, dY)
+    x2, dy2 = X.clone(), dY.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both(x2, dy2)
+    for seed in (5, 6):
+        x2.copy_(torch.randn(M, K).to(torch.bfloat16))
+        dy2.copy_(grads(M, K, seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, both(x2, dy2)))
+    _, Wp, gamma, _, q, s = layer(200, 320, 1003, 1)
+    dz = grads(200, 1003, 2)
+    want = (both(X, dY), bl.bl_backward_weight(dz, q, s), bl.bl_backward_input(dz, Wp, gamma, 320))
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(a):
+            r1 = both(X, dY)
+            r3 = bl.bl_backward_input(dz, Wp, gamma, 320)
+        with torch.cuda.stream(b):
+            r2 = bl.bl_backward_weight(dz, q, s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(r1, want[0]))
+        assert torch.equal(r2, want[1]) and torch.equal(r3, want[2])
+
+
+def test_one_tokens_training_step_and_reused_rows():
+    # rows of a larger buffer (16-byte aligned rows are enough), the same buffer twice
+    K, N = 192, 72
+    _, Wp, gamma, C, _, _ = layer(4, K, N, 1)
+    big = torch.randn(9, K).to(torch.bfloat16).cuda()
+    for m in (0, 5, 8):
+        X = big[m:m + 1]
+        Y, q, s, stat = bl.bl_forward_checkpoint(X, Wp, gamma, N, norm=bl.BL_NORM_RMS)
+        dY = grads(1, N, m)
+        dXn = bl.bl_backward_input(dY, Wp, gamma, K)
+        check_dx(dXn, dY, C, gamma)
+        check_dw(bl.bl_backward_weight(dY, q, s), dY, q, s)
+    # X as its own gradient: the same tensor as both arguments
+    X = torch.randn(6, K).to(torch.bfloat16).cuda()
+    _, _, stat = bl.bl_norm_forward(X, bl.BL_NORM_RMS)
+    dX, _, _ = bl.bl_norm_backward(X, X, bl.BL_NORM_RMS, stat)
+    x = X.to(F64)
+    rs = (stat.to(F64) + EPS).rsqrt()[:, None]
+    xh = x * rs
+    want = (x - xh * (x * xh).mean(1, keepdim=True)) * rs
+    terms = (x.abs() + xh.abs() * (x * xh).abs().mean(1, keepdim=True)) * rs
+    assert worst(dX, want, 2.0**-8 * want.abs() + (fp32_err(K) + 2.0**-20) * terms) <= 1.0
