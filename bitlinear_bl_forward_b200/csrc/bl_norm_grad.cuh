@@ -18,10 +18,10 @@
 
 #include "bl_act.cuh"
 #include "bl_common.cuh"
-#include "bl_tc_common.cuh"
 
 namespace bl {
 
+constexpr unsigned int kSiteNormRows = 8;   // wait-site identifier (see bl_tc_common.cuh)
 constexpr int kNgSms = 148;           // CTAs of the weight gradient's partial rows: a multiple of the SMs
 constexpr int kNgRowMaxK = 8192;      // widest row whose weight gradient stays in registers
 

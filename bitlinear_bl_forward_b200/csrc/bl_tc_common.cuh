@@ -19,7 +19,6 @@ enum : unsigned int {
   kSiteAcc = 5,
   kSiteDrain = 6,
   kSiteProbe = 7,
-  kSiteNormRows = 8,
   kSiteSelftest = 0xEE
 };
 

@@ -731,3 +731,48 @@ def forward_layernorm(x_bits: np.ndarray, W: np.ndarray, eps: float = 1e-5, bits
     out = forward(nrm["xn"], W, bits)
     out.update({k: nrm[k] for k in ("mean", "var", "r", "xn")})
     return out
+
+
+# ---------------------------------------------------------------------------
+# Training: straight-through gradients and the norm's backward, in float64.
+#
+# The pages train with the straight-through estimator (round and clip have
+# derivative one); the scales gamma and s_m are constants.
+# ---------------------------------------------------------------------------
+
+def grad_input(dy: np.ndarray, codes: np.ndarray, gamma: np.float32) -> np.ndarray:
+    """dX = dY (gamma C): dy [M, N], codes [N, K] -> [M, K]."""
+    return np.asarray(dy, dtype=np.float64) @ (np.asarray(codes, dtype=np.float64) * float(gamma))
+
+
+def grad_weight(dy: np.ndarray, q: np.ndarray, s: np.ndarray) -> np.ndarray:
+    """dW = dY^T (q / s): dy [M, N], q [M, K], s [M] -> [N, K]."""
+    xh = np.asarray(q, dtype=np.float64) / np.asarray(s, dtype=np.float64)[:, None]
+    return np.asarray(dy, dtype=np.float64).T @ xh
+
+
+def norm_plain(x: np.ndarray, layer: bool, weight=None, bias=None, eps: float = 1e-5):
+    """LayerNorm (layer) or RMSNorm of rows: (y, mean or None, stat), stat the
+    biased variance or the mean of squares."""
+    x = np.asarray(x, dtype=np.float64)
+    mean = x.mean(axis=1) if layer else None
+    d = x - mean[:, None] if layer else x
+    stat = (d * d).mean(axis=1)
+    y = d / np.sqrt(stat + eps)[:, None]
+    if weight is not None:
+        y = y * np.asarray(weight, dtype=np.float64)
+    if bias is not None:
+        y = y + np.asarray(bias, dtype=np.float64)
+    return y, mean, stat
+
+
+def norm_grad(dy: np.ndarray, xh: np.ndarray, stat: np.ndarray, layer: bool, weight=None, eps: float = 1e-5):
+    """Gradients of norm_plain from the normalised rows xh: (dx, dweight, dbias)."""
+    dy = np.asarray(dy, dtype=np.float64)
+    xh = np.asarray(xh, dtype=np.float64)
+    g = dy if weight is None else dy * np.asarray(weight, dtype=np.float64)
+    dx = g - xh * (g * xh).mean(axis=1, keepdims=True)
+    if layer:
+        dx = dx - g.mean(axis=1, keepdims=True)
+    dx = dx / np.sqrt(np.asarray(stat, dtype=np.float64) + eps)[:, None]
+    return dx, (dy * xh).sum(axis=0), dy.sum(axis=0)
