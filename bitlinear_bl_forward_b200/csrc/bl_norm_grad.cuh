@@ -104,10 +104,10 @@ __device__ __forceinline__ uint32_t f2_pack_bf16(f2 a) {
   return r;
 }
 
-// 1 / sqrt(stat + eps): one rounding each.
-__device__ __forceinline__ float norm_rstd(float stat, float eps) {
-  return __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(stat, eps)));
-}
+// 1 / sqrt(stat + eps), within two ulp (rsqrtf).  Every thread of a row forms it:
+// a correctly rounded root and quotient would be a fifth of the backward's
+// instructions.
+__device__ __forceinline__ float norm_rstd(float stat, float eps) { return rsqrtf(__fadd_rn(stat, eps)); }
 
 // One row per CTA.  X and Y may be the same buffer (a thread writes only the
 // chunks it has read), so neither is __restrict__.

@@ -607,3 +607,59 @@ def test_one_tokens_training_step_and_reused_rows():
     want = (x - xh * (x * xh).mean(1, keepdim=True)) * rs
     terms = (x.abs() + xh.abs() * (x * xh).abs().mean(1, keepdim=True)) * rs
     assert worst(dX, want, 2.0**-8 * want.abs() + (fp32_err(K) + 2.0**-20) * terms) <= 1.0
+
+
+@pytest.mark.parametrize("M,K", [(1, 64), (37, 2560), (40, 4160), (9, 8192), (11, 8256)])
+def test_norm_weight_gradients_alone(M, K):
+    # the C entry with dX not wanted, and each of dweight and dbias alone
+    L = bl.lib()
+    X, dY = torch.randn(M, K).to(torch.bfloat16).cuda(), grads(M, K, 1)
+    w = torch.randn(K).to(torch.bfloat16).cuda()
+    _, mean, stat = bl.bl_norm_forward(X, bl.BL_NORM_LAYER, weight=w)
+    _, dw, db = bl.bl_norm_backward(dY, X, bl.BL_NORM_LAYER, stat, mean=mean, weight=w, need_bias=True)
+    need = bl.bl_norm_backward_workspace_bytes(M, K)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    for want_w, want_b in ((1, 1), (1, 0), (0, 1)):
+        gw, gb = Guarded((K,), torch.float32), Guarded((K,), torch.float32)
+        assert L.bl_norm_backward(dY.data_ptr(), X.data_ptr(), w.data_ptr(), bl.BL_NORM_LAYER, EPS, mean.data_ptr(),
+                                  stat.data_ptr(), M, K, 0, None, gw.t.data_ptr() if want_w else None,
+                                  gb.t.data_ptr() if want_b else None, ws.data_ptr(), need, st) == 0
+        assert gw.intact() and gb.intact()
+        assert not want_w or torch.equal(gw.t, dw)
+        assert not want_b or torch.equal(gb.t, db)
+
+
+def test_widest_rows_and_offsets_past_32_bits():
+    # K = 65536; outputs and inputs of more than 2^31 elements, checked at both ends
+    K = 65536
+    g = torch.Generator(device="cuda").manual_seed(0)
+    M, N = 70, 33001
+    q = torch.randint(-127, 128, (M, K), generator=g, device="cuda").to(torch.int8)
+    s = torch.rand(M, generator=g, device="cuda") + 1
+    dY = (torch.randn(M, N, generator=g, device="cuda") * 1e-3).to(torch.bfloat16)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.zeros(N, K, dtype=dtype, device="cuda")
+        bl.bl_backward_weight(dY, q, s, out=out, accumulate=True)
+        for a, b in ((0, 40), (N - 40, N)):
+            check_dw(out[a:b], dY[:, a:b], q, s)
+        del out
+    del q, dY
+    M, N = 33001, 24
+    Wp = torch.randint(0, 256, (N, K // 4), generator=g, device="cuda").to(torch.uint8)
+    Wp = torch.where((Wp & (Wp >> 1) & 0x55) != 0, Wp & 0x55, Wp)   # no field is 3
+    gamma = torch.full((1,), 0.02, device="cuda")
+    C = bl.bl_unpack_weights(Wp, N, K).to(F64)
+    dY = (torch.randn(M, N, generator=g, device="cuda") * 1e-3).to(torch.bfloat16)
+    dX = bl.bl_backward_input(dY, Wp, gamma, K)
+    for a, b in ((0, 40), (M - 40, M)):
+        check_dx(dX[a:b], dY[a:b], C, gamma)
+    # the norm of those 33001 rows, forward and back
+    Y, mean, stat = bl.bl_norm_forward(dX, bl.BL_NORM_LAYER)
+    b = slice(M - 20, M)
+    mu, var, d = norm_ref(dX[b], bl.BL_NORM_LAYER)
+    e = fp32_err(K)
+    mag = dX[b].to(F64).abs().mean(1)
+    assert worst(stat[b], var, (e + 2.0**-20) * var + 2 * (e * mag).square()) <= 1.0
+    dZ, _, db = bl.bl_norm_backward(Y, dX, bl.BL_NORM_LAYER, stat, mean=mean, need_bias=True, out=Y)
+    assert dZ is Y and torch.isfinite(dZ[b].float()).all() and torch.isfinite(db).all()
