@@ -1619,7 +1619,7 @@ struct GradPlan {
   size_t pad_bytes, part_bytes;
 };
 
-constexpr int kGradPlanPairs = 74;   // CTA pairs of a B200
+constexpr unsigned kGradPlanPairs = 74;   // CTA pairs of a B200
 
 // Tiles of 256 k by bn r on 74 CTA pairs, and the number of parts of the sum:
 // whichever takes least by this model of the kernel, in us.
@@ -1644,23 +1644,26 @@ GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N, bool bf16_out) {
   const int64_t R = kind == bl::kGradInput ? M : N, L = kind == bl::kGradInput ? N : M;
   const int64_t kt = (K + 2 * bl::kGtK - 1) / (2 * bl::kGtK);
   const Shape* shapes = kind == bl::kGradInput ? input : bf16_out ? weight16 : weight32;
+  // (32-bit counts: R and L are below 2^31; this runs twice a call)
+  const unsigned r32 = static_cast<unsigned>(R), l32 = static_cast<unsigned>(L), kt32 = static_cast<unsigned>(kt);
+  const double part_us = static_cast<double>(R) * static_cast<double>(K) * 1e-6;
   double best = 1e300;
   for (int b = 0; b < (kind == bl::kGradInput ? 5 : 3); ++b) {
-    const int bn = shapes[b].bn, bc = bl::gt_bc(kind, bn);
-    const int64_t rt = (R + bn - 1) / bn, tiles = kt * rt, nk = (L + bc - 1) / bc;
+    const unsigned bn = shapes[b].bn, bc = bl::gt_bc(kind, shapes[b].bn);
+    const unsigned rt = (r32 + bn - 1) / bn, tiles = kt32 * rt, nk = (l32 + bc - 1) / bc;
     const double stage = shapes[b].stage * (bc / 64);
-    const int64_t fill = std::max<int64_t>(1, kGradPlanPairs / tiles);
-    const int64_t tries[6] = {1, 2, 3, 4, fill, 2 * fill};
+    const unsigned fill = tiles < kGradPlanPairs ? kGradPlanPairs / tiles : 1u, most = nk / 2 > 1 ? nk / 2 : 1u;
+    const unsigned tries[6] = {1, 2, 3, 4, fill, 2 * fill};
     for (int j = 0; j < (tiles > 4 * kGradPlanPairs ? 1 : 6); ++j) {
-      const int64_t want = std::min<int64_t>(tries[j], std::max<int64_t>(1, nk / 2));
-      const int64_t per = (nk + want - 1) / want, splits = (nk + per - 1) / per;
-      const int64_t waves = (tiles * splits + kGradPlanPairs - 1) / kGradPlanPairs;
-      double t = static_cast<double>(waves) * std::max(static_cast<double>(per) * stage, shapes[b].epilogue) +
-                 shapes[b].epilogue;
-      if (splits > 1) t += 2.5 + static_cast<double>(splits) * R * K * 8 / 8e6;
+      if (j > 0 && tries[j] > most && tries[j - 1] >= most) continue;   // the same cut again
+      const unsigned want = tries[j] < most ? tries[j] : most;
+      const unsigned per = (nk + want - 1) / want, splits = (nk + per - 1) / per;
+      const unsigned waves = (tiles * splits + kGradPlanPairs - 1) / kGradPlanPairs;
+      double t = waves * std::max(per * stage, shapes[b].epilogue) + shapes[b].epilogue;
+      if (splits > 1) t += 2.5 + splits * part_us;
       if (t < best) {
         best = t;
-        g.bn = bn;
+        g.bn = static_cast<int>(bn);
         g.rt = static_cast<int>(rt);
         g.per = static_cast<int>(per);
         g.splits = static_cast<int>(splits);
