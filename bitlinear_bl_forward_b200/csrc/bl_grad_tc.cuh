@@ -28,10 +28,24 @@
 // bl_grad_join_kernel in a fixed order.
 // The tensor core truncates when it adds to an fp32 accumulator, so the error
 // of a long sum grows with its length instead of its root: 1.0e-5 of the norm
-// over 4096 tokens, where rounding would leave 1e-6 (measured).  An fp32
-// result is therefore summed in segments of 1024 tokens, which the epilogue
-// adds up with rounding: the pair that owns the tile stores the first and adds
-// the others to its own output, which is still in L2.
+// over 4096 tokens, hi + lo included (measured).  An fp32 result is therefore
+// summed in segments of 2048 tokens, which the epilogue adds up with rounding
+// (5.3e-6; a plain fp32 product: 1.1e-6): the pair that owns the tile stores the
+// first segment and adds the others to its own output, which is still in L2.
+// Segments of 1024 tokens cost 3% more.
+//
+// What bounds it.  Per 64 rows of the sum and CTA, at BN = 256: 512 clocks of
+// tensor work a term, against what passes through 128 bytes a clock of shared
+// memory: A written and read (32 KB a term), dY in and read (32 KB, the read once
+// a term), the raw rows in and out (4 or 16 KB).  That is 530 clocks for the
+// input gradient, 640 for a bf16 and 1000 (of 1024) for an fp32 weight gradient.
+// At BN <= 128 A's way through shared memory alone is 256 of them for 256 clocks of
+// tensor work or less.  Measured (B200): 2B down projection, M = 4096, 91 us alone
+// (1.59 PFLOP/s, the tensor pipe 83% active), 110 us in a seconds-long run under
+// the power cap (1.31); 2B up projection's fp32 gradient 190 and 225 us (twice
+// 0.76 PFLOP/s; pipe 92% active while a pair works, four waves for 3.65);
+// 4-bit-activation layer's bf16 gradient 142 and 158 us (1.30; pipe 74%); 70B-class
+// layer with 128 tokens 57 us (1.05; pipe 61%, DRAM 14%).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -68,10 +82,10 @@ struct GtCfg {
   static constexpr int kASlotBytes = TERMS * kTileBytes;
   // Converter warps work in groups of four, each group on a stage of its own,
   // so that a stage's latency (waits, loads, conversion, proxy fence, arrival:
-  // about 1000 clocks) overlaps the others'.  Measured on the 2B layers with 2,
-  // 3 and 4 groups: input 97, 91, - us; weight fp32 191, 191, 193; weight bf16
-  // 162, 150, 143 (half the tensor work beside the same loads); eight warps a
-  // group are slower (fp32 193, bf16 157).
+  // about 1000 clocks) overlaps the others'.  Measured on the 2B layers and the
+  // 4-bit-activation layer with 2, 3 and 4 groups: input 97, 91, 91 us; weight
+  // fp32 191, 191, 193; weight bf16 162, 150, 143 (half the tensor work beside the
+  // same loads); two groups of eight warps are slower (fp32 193, bf16 157).
   static constexpr int kGroupWarps = 4;
   static constexpr int kGroups = KIND == kGradInput || TERMS == 2 ? 3 : 4;
   static constexpr int kFirstEpi = 2 + kGroupWarps * kGroups;
@@ -79,11 +93,10 @@ struct GtCfg {
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;       // r of one epilogue step
   static constexpr int kOutBytes = TERMS == 2 ? 4096 : 2048;   // staging a warp: tiles of [32 r][32 k] bf16 or [16 r][32 k] fp32
   static constexpr int kOutTotal = kGtEpiWarps * kOutBytes;
-  static constexpr int kASlots = kBC == 128 || TERMS == 2 ? 3 : 4;   // being expanded, and one being read
+  static constexpr int kASlots = kBC == 128 || TERMS == 2 ? 3 : 4;   // expanded operand tiles in flight
   static constexpr int kBudget = 227 * 1024 - 1024 - 512 - kOutTotal - kASlots * kASlotBytes;
   static constexpr int kMaxStages = kBudget / kInBytes;
   static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
-  static constexpr int kAOffset = 0;
   static constexpr int kInOffset = kASlots * kASlotBytes;
   static constexpr int kSegment = TERMS == 2 ? kGtSegment / kBC : 1 << 30;
   static constexpr int kOutOffset = kInOffset + kStages * kInBytes;
