@@ -70,6 +70,23 @@ constexpr int kQNumBars = 2 * kQStages + kQASlots + 5;
 constexpr int kQEpiOffset = kQBarOffset + kQNumBars * 8 + 16;
 constexpr int kQSmemBytes = kQEpiOffset + 2 * kQBN * 8 + 1024;
 
+// One lane of a converged warp, chosen by the hardware (the same one every
+// time): the branch it guards stays warp-uniform for the compiler, so that
+// descriptors, addresses and coordinates live in uniform registers.  Behind a
+// lane == 0 branch the gradient kernel's four MMAs took 450 clocks to issue and a
+// stage's two TMA loads 490, beside 512 clocks of tensor work; here the 70B-class
+// layer with 2048 tokens went from 320 to 292 us.  A decision to leave a loop is
+// taken by the whole warp: elect.sync names all its lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // One weight tensor of a launch.  A launch serves one or two problems that
 // share the quantised activations (e.g. the up and gate projections of a
 // feed-forward block): its tiles run over the weight rows of problem 0 then
@@ -144,44 +161,48 @@ __global__ void __launch_bounds__(kQThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    // ---------------- TMA producer (both CTAs) ----------------
-    if (lane == 0) {
+    // ---------------- TMA producer (both CTAs; the whole warp, one lane issues) ----------------
+    if (elect_one()) {
       prefetch_tmap(&tmX);
       prefetch_tmap(&P.p[0].tmW);
       if (P.count > 1) prefetch_tmap(&P.p[1].tmW);
-      uint32_t g = 0;
-      bool stop = false;
-      for (int tile = pair; tile < ntiles && !stop; tile += npairs) {
-        const int m0 = (tile % mt) * kQBN + static_cast<int>(rank) * kQHalf;
-        const int nt = tile / mt, w = nt >= ntn0 ? 1 : 0;
-        const int n0 = (nt - (w ? ntn0 : 0)) * kQRows + static_cast<int>(rank) * kTcRows;
-        const CUtensorMap* tmW = &P.p[w].tmW;
-        for (int ks = 0; ks < nk; ++ks, ++g) {
-          const int s = g % S;
-          if (g >= static_cast<uint32_t>(S) &&
-              !mbar_wait_cluster(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty)) {
-            stop = true;
-            break;
-          }
+    }
+    uint32_t g = 0;
+    int s = 0;
+    bool stop = false;
+    for (int tile = pair; tile < ntiles && !stop; tile += npairs) {
+      const int m0 = (tile % mt) * kQBN + static_cast<int>(rank) * kQHalf;
+      const int nt = tile / mt, w = nt >= ntn0 ? 1 : 0;
+      const int n0 = (nt - (w ? ntn0 : 0)) * kQRows + static_cast<int>(rank) * kTcRows;
+      const CUtensorMap* tmW = &P.p[w].tmW;
+      for (int ks = 0; ks < nk; ++ks, ++g) {
+        if (g >= static_cast<uint32_t>(S) &&
+            !__all_sync(0xffffffffu,
+                        mbar_wait_cluster(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty))) {
+          stop = true;
+          break;
+        }
+        if (elect_one()) {
           mbar_arrive_expect_tx(&full[s], kQStageBytes);
 #pragma unroll
           for (int bx = 0; bx < kQBK / 128; ++bx)
             tma_load_2d(sX + s * kQXStageBytes + bx * kQXBoxBytes, &tmX, ks * kQBK + bx * 128, m0, &full[s]);
           tma_load_2d(sW + s * kQWStageBytes, tmW, ks * (kQBK / 4), n0, &full[s]);
         }
-      }
-      const uint32_t issued = g;
-      for (uint32_t s = 0; s < static_cast<uint32_t>(S) && s < issued; ++s) {
-        const uint32_t last = s + S * ((issued - 1 - s) / S);
-        mbar_wait(&full[s], (last / S) & 1, nullptr, limit_ns, kSiteDrain);
+        if (++s == S) s = 0;
       }
     }
+    const uint32_t issued = g;
+    for (uint32_t t = 0; t < static_cast<uint32_t>(S) && t < issued; ++t) {
+      const uint32_t last = t + S * ((issued - 1 - t) / S);
+      mbar_wait(&full[t], (last / S) & 1, nullptr, limit_ns, kSiteDrain);
+    }
   } else if (warp == 1) {
-    // ---------------- MMA issuer (leader only) ----------------
-    if (lane == 0 && rank == 0) {
+    // ---------------- MMA issuer (leader only; the whole warp, one lane issues) ----------------
+    if (rank == 0) {
       const uint32_t idesc = idesc_i8(kQRows, kQBN);
-      // ring positions kept as counters: this thread's instruction count
-      // bounds the MMA rate
+      // ring positions kept as counters: this warp's instruction count bounds
+      // the MMA rate
       const uint32_t dlo0 = desc_sw128_lo(smem_u32(sX));
       int s = 0, t = 0;
       uint32_t tph = 0;   // phase parity of afull[t]
@@ -189,11 +210,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
       bool stop = false;
       for (int tile = pair; tile < ntiles && !stop; tile += npairs, ++i) {
         const int b = i & 1;
-        if (i >= 2 && !mbar_wait_cluster(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc)) break;
+        if (i >= 2 &&
+            !__all_sync(0xffffffffu,
+                        mbar_wait_cluster(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc)))
+          break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + b * kQAccCols;
         for (int ks = 0; ks < nk; ++ks) {
-          if (!mbar_wait_cluster(&afull[t], tph, abort_flag, limit_ns, kSiteMmaExfull)) {
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster(&afull[t], tph, abort_flag, limit_ns, kSiteMmaExfull))) {
             stop = true;
             break;
           }
@@ -201,10 +225,12 @@ __global__ void __launch_bounds__(kQThreads, 1)
           // the stage's 16 MMAs (K = 32 each) from one asm block: MMA k reads
           // A column 8k of the slot and token box k / 4, bytes 32 (k % 4)
           static_assert(kQBK == 512, "one stage is sixteen MMAs");
-          mma_i8_stage16_pair<kQXBoxBytes / 16>(d_tmem, tmem + kQACol + kQASlotCols * t,
-                                                dlo0 + s * (kQXStageBytes / 16), kDescSw128Hi, idesc,
-                                                ks != 0 ? 1u : 0u);
-          tc_commit_pair(&done[s], 3);
+          if (elect_one()) {
+            mma_i8_stage16_pair<kQXBoxBytes / 16>(d_tmem, tmem + kQACol + kQASlotCols * t,
+                                                  dlo0 + s * (kQXStageBytes / 16), kDescSw128Hi, idesc,
+                                                  ks != 0 ? 1u : 0u);
+            tc_commit_pair(&done[s], 3);
+          }
           if (++s == S) s = 0;
           if (++t == kQASlots) {
             t = 0;
@@ -212,10 +238,10 @@ __global__ void __launch_bounds__(kQThreads, 1)
           }
         }
         if (stop) break;
-        tc_commit_pair(&accfull[b], 3);
+        if (elect_one()) tc_commit_pair(&accfull[b], 3);
       }
       // no MMA of the pair may be in flight when either CTA frees its TMEM
-      tc_commit_pair(drain, 1);
+      if (elect_one()) tc_commit_pair(drain, 1);
       mbar_wait(drain, 0, nullptr, limit_ns, kSiteDrain);
     }
   } else if (warp < kQFirstEpi) {

@@ -51,6 +51,7 @@
 #include <cuda_bf16.h>
 
 #include "bl_common.cuh"
+#include "bl_gemm_2sm.cuh"
 #include "bl_grad.cuh"
 #include "bl_tc_common.cuh"
 
@@ -180,21 +181,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
-}
-
-// One lane of a converged warp, chosen by the hardware (the same one every
-// time): the branch it guards stays warp-uniform for the compiler, so that
-// descriptors, addresses and coordinates live in uniform registers.  Behind a
-// lane == 0 branch four MMAs took 450 clocks to issue and a stage's two TMA
-// loads 490; 512 clocks is the tensor work of a stage.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
 }
 
 // Arrive on CTA 0's copy of a barrier after generic shared-memory writes that
