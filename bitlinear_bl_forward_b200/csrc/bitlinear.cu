@@ -1592,6 +1592,15 @@ namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether [a, a + na) and [b, b + nb) share a byte (null ranges do not).
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+// As above, but the same range is fine (a row is read before it is written).
+bool overlaps_partly(const void* a, const void* b, size_t n) { return a != b && overlaps(a, n, b, n); }
+
 bl_status check_rows(int64_t M, int64_t K) {
   if (K <= 0 || (K % 64) != 0 || K > kMaxK) return BL_ERR_SHAPE;
   return check_m(M, K);
@@ -1937,6 +1946,10 @@ bl_status bl_forward_checkpoint(const uint16_t* X, int norm, float eps, int64_t 
     return BL_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < bl_forward_checkpoint_workspace_bytes(M, K, N, bits)) return BL_ERR_WORKSPACE;
   if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
+  const size_t x_bytes = static_cast<size_t>(M) * K * 2, q_bytes = static_cast<size_t>(M) * K;
+  const size_t y_bytes = static_cast<size_t>(M) * N * 2;
+  if (overlaps(Y, y_bytes, X, x_bytes) || overlaps(Xq, q_bytes, X, x_bytes) || overlaps(Y, y_bytes, Xq, q_bytes))
+    return BL_ERR_INVALID_ARG;
   const int Q = bits == 8 ? 127 : 7;
   const int m = static_cast<int>(M), k = static_cast<int>(K);
   int* R = static_cast<int*>(workspace);
@@ -1970,6 +1983,10 @@ bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
     if (!workspace || workspace_bytes < need) return BL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
   }
+  const size_t dx_bytes = static_cast<size_t>(M) * K * 2;
+  if (overlaps(dX, dx_bytes, dY, static_cast<size_t>(M) * N * 2) ||
+      overlaps(dX, dx_bytes, Wp, static_cast<size_t>(N) * K / 4))
+    return BL_ERR_INVALID_ARG;
   bl::GradArgs a = {};
   a.dY = dY;
   a.A = Wp;
@@ -2009,6 +2026,9 @@ bl_status bl_backward_weight(const uint16_t* dY, const int8_t* Xq, const float* 
     if (!workspace || workspace_bytes < need) return BL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
   }
+  const size_t dw_bytes = static_cast<size_t>(N) * K * ((flags & BL_GRAD_BF16) ? 2 : 4);
+  if (overlaps(dW, dw_bytes, dY, static_cast<size_t>(M) * N * 2) || overlaps(dW, dw_bytes, Xq, static_cast<size_t>(M) * K))
+    return BL_ERR_INVALID_ARG;
   bl::GradArgs a = {};
   a.dY = dY;
   a.A = reinterpret_cast<const uint8_t*>(Xq);
@@ -2033,6 +2053,7 @@ bl_status bl_norm_forward(const uint16_t* X, const uint16_t* weight, const uint1
   if (!X || !Y) return BL_ERR_INVALID_ARG;
   if (!aligned16(X) || !aligned16(Y) || !aligned16(weight) || !aligned16(bias) || !aligned4(mean) || !aligned4(stat))
     return BL_ERR_ALIGNMENT;
+  if (overlaps_partly(X, Y, static_cast<size_t>(M) * K * 2)) return BL_ERR_INVALID_ARG;
   const int m = static_cast<int>(M), k = static_cast<int>(K);
   if (norm == BL_NORM_LAYER) return launch_norm_fwd<true>(X, weight, bias, eps, m, k, Y, mean, stat, stream);
   return launch_norm_fwd<false>(X, weight, bias, eps, m, k, Y, nullptr, stat, stream);
@@ -2068,6 +2089,9 @@ bl_status bl_norm_backward(const uint16_t* dY, const uint16_t* X, const uint16_t
     if (!workspace || workspace_bytes < bl_norm_backward_workspace_bytes(M, K)) return BL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
   }
+  const size_t row_bytes = static_cast<size_t>(M) * K * 2, w_bytes = static_cast<size_t>(K) * sizeof(float);
+  if (overlaps_partly(dX, dY, row_bytes) || overlaps_partly(dX, X, row_bytes) || overlaps(dweight, w_bytes, dbias, w_bytes))
+    return BL_ERR_INVALID_ARG;
   bl::NormGradArgs a = {};
   a.dY = dY;
   a.X = X;
@@ -2094,6 +2118,9 @@ bl_status bl_norm_backward_checkpoint(const uint16_t* dXn, const int8_t* Xq, con
   if (!dXn || !Xq || !scale || !stat || !dX) return BL_ERR_INVALID_ARG;
   if (!aligned16(dXn) || !aligned16(Xq) || !aligned16(dX) || !aligned4(scale) || !aligned4(stat))
     return BL_ERR_ALIGNMENT;
+  const size_t row_bytes = static_cast<size_t>(M) * K * 2;
+  if (overlaps_partly(dX, dXn, row_bytes) || overlaps(dX, row_bytes, Xq, static_cast<size_t>(M) * K))
+    return BL_ERR_INVALID_ARG;
   bl::NormGradArgs a = {};
   a.dY = dXn;
   a.Xq = Xq;

@@ -425,6 +425,10 @@ BL_API bl_status bl_forward_norm_grouped(int count, const bl_linear* problems, i
  * the two passes is M*K bytes of codes and 4*M bytes of scales, half of the
  * bf16 activations, and it is exactly what the forward multiplied.
  * Values of dY that are NaN or Inf give undefined (but memory-safe) results.
+ * Outputs that overlap an input return BL_ERR_INVALID_ARG, but for the rows that
+ * a norm may take in place (exactly the same range).  A workspace is clobbered:
+ * calls that may overlap on the GPU (streams, graphs replayed at once) need one
+ * each.  Outputs are written after the kernels before the call on its stream.
  * ------------------------------------------------------------------------- */
 
 /*

@@ -663,3 +663,34 @@ def test_widest_rows_and_offsets_past_32_bits():
     assert worst(stat[b], var, (e + 2.0**-20) * var + 2 * (e * mag).square()) <= 1.0
     dZ, _, db = bl.bl_norm_backward(Y, dX, bl.BL_NORM_LAYER, stat, mean=mean, need_bias=True, out=Y)
     assert dZ is Y and torch.isfinite(dZ[b].float()).all() and torch.isfinite(db).all()
+
+
+@pytest.mark.parametrize("norm", [bl.BL_NORM_RMS, bl.BL_NORM_LAYER])
+def test_a_step_behind_a_norm_with_parameters(norm):
+    """Norm with weight (and bias), checkpointed linear, and back: the chain of
+    calls, its norm part against 64 bits from the calls' own dXn."""
+    M, K, N = 67, 320, 130
+    g = torch.Generator().manual_seed(4)
+    X = torch.randn(M, K, generator=g).to(torch.bfloat16).cuda()
+    w = (1 + 0.2 * torch.randn(K, generator=g)).to(torch.bfloat16).cuda()
+    la = norm == bl.BL_NORM_LAYER
+    b = (0.2 * torch.randn(K, generator=g)).to(torch.bfloat16).cuda() if la else None
+    _, Wp, gamma, C, _, _ = layer(4, K, N, 1)
+    Xn, mean, stat = bl.bl_norm_forward(X, norm, weight=w, bias=b, eps=EPS)
+    Y, q, s, _ = bl.bl_forward_checkpoint(Xn, Wp, gamma, N)
+    assert torch.equal(Y, bl.bl_forward(Xn, Wp, gamma, N))
+    dY = grads(M, N, 5)
+    dXn = bl.bl_backward_input(dY, Wp, gamma, K)
+    check_dx(dXn, dY, C, gamma)
+    check_dw(bl.bl_backward_weight(dY, q, s), dY, q, s)
+    dX, dw, db = bl.bl_norm_backward(dXn, X, norm, stat, mean=mean, weight=w, need_bias=la, eps=EPS)
+    rs = (stat.to(F64) + EPS).rsqrt()[:, None]
+    xh = (X.to(F64) - (mean.to(F64)[:, None] if la else 0.0)) * rs
+    dy = dXn.to(F64)
+    gg = dy * w.to(F64)
+    want = (gg - xh * (gg * xh).mean(1, keepdim=True) - (gg.mean(1, keepdim=True) if la else 0.0)) * rs
+    terms = (gg.abs() + xh.abs() * (gg * xh).abs().mean(1, keepdim=True) + gg.abs().mean(1, keepdim=True)) * rs
+    assert worst(dX, want, 2.0**-8 * want.abs() + (fp32_err(K) + 2.0**-20) * terms + 1e-300) <= 1.0
+    em = 2.0**-24 * (M + 16)
+    assert worst(dw, (dy * xh).sum(0), em * (dy * xh).abs().sum(0) + 1e-300) <= 1.0
+    assert (db is not None) == la and (db is None or worst(db, dy.sum(0), em * dy.abs().sum(0) + 1e-300) <= 1.0)

@@ -207,3 +207,23 @@ def test_binding_refuses_host_tensors():
         bl.bl_norm_backward_checkpoint(x, q, g, bl.BL_NORM_RMS, g)
     with pytest.raises(TypeError):
         bl.bl_norm_forward(torch.zeros(64), bl.BL_NORM_RMS)
+
+
+def test_overlaps_are_refused(L):
+    B = 0x1000000
+    # dX over dY or the weights; dW over dY or the codes
+    assert L.bl_backward_input(B, 4, 64, 64, A, A, B, A, BIG, None) == INVALID
+    assert L.bl_backward_input(B, 4, 64, 64, A, A, B + 4 * 64 * 2 - 16, A, BIG, None) == INVALID
+    assert L.bl_backward_input(A, 4, 64, 64, B, A, B - 16, A, BIG, None) == INVALID
+    assert L.bl_backward_weight(B, A, A, 4, 64, 8, 0, B + 16, A, BIG, None) == INVALID
+    assert L.bl_backward_weight(A, B, A, 4, 64, 8, 2, B - 8 * 64 * 2 + 16, A, BIG, None) == INVALID
+    # a norm's rows in place only as a whole
+    assert L.bl_norm_forward(B, None, None, 1, 1e-5, 4, 64, B + 128, None, None, None) == INVALID
+    assert L.bl_norm_backward(B, A, None, 0, 1e-5, None, A, 4, 64, 0, B + 16, None, None, None, 0, None) == INVALID
+    assert L.bl_norm_backward(A, B, None, 0, 1e-5, None, A, 4, 64, 0, B - 16, None, None, None, 0, None) == INVALID
+    assert L.bl_norm_backward(A, B, None, 0, 1e-5, None, A, 4, 64, 0, None, B, B, A, BIG, None) == INVALID
+    assert L.bl_norm_backward_checkpoint(B, A, A, 1, 1e-5, A, 4, 64, B + 16, None) == INVALID
+    assert L.bl_norm_backward_checkpoint(A, B, A, 1, 1e-5, A, 4, 64, B, None) == INVALID
+    # the checkpoint's outputs over its input or over one another
+    for Y, q in ((B, A), (A, B + 16), (B + 4096, B + 4112)):
+        assert L.bl_forward_checkpoint(B, 2, 1e-5, 4, 64, 8, A, A, 8, Y, q, A, None, A, BIG, None) == INVALID
