@@ -1623,66 +1623,83 @@ bl_status check_mnk(int64_t M, int64_t N, int64_t K) {
 struct GradPlan {
   int bn;                // r of a tile
   int kt, rt;            // tiles along k and r
-  int splits, per;       // parts of the sum, stages a part
+  bl::GtCut cut;         // chunks of the tiles' sums
+  int parts;             // most parts of a tile (1: written directly)
   int64_t ld;            // row stride of dY in elements (N, or a padded copy's)
   size_t pad_bytes, part_bytes;
 };
 
 constexpr unsigned kGradPlanPairs = 74;   // CTA pairs of a B200
 
-// Tiles of 256 k by bn r on 74 CTA pairs, and the number of parts of the sum:
-// whichever takes least by this model of the kernel, in us.
+// Tiles of 256 k by bn r on 74 CTA pairs, and how their sums are cut: whole
+// tiles, every tile in the same number of parts, or the stages of all tiles dealt
+// out evenly to the pairs.  Whichever takes least by this model of the kernel, in
+// us:
 //   * 64 rows of the sum take `stage`, about the same for every bn up to 128
 //     (there the expanded operand's way through shared memory is the limit);
-//   * pairs work in waves of whole items; a wave is as long as its sums, or as
-//     its epilogues where those are longer (few rows);
+//   * pairs work in waves of chunks; a wave is as long as its sums, or as its
+//     epilogues where those are longer (few rows);
 //   * parts are written and read once more, and need a second launch.
 // Both sides measured: the 2B down projection's input gradient at bn = 256
-// takes 93 us, at 192 more; the up projection's (4096 x 2560 out) takes 105 us at
-// 192 (three waves) where 256 needs three of its longer ones; 300 tokens take
-// 20 us at 128 in two parts, 26 in one, 38 at 256.
+// takes 91 us; the up projection's (4096 x 2560 out) 105 us at 192 (three waves)
+// where 256 needs three of its longer ones (150, before the last steps); 300
+// tokens take 20 us at 128 in two parts, 26 in one, 38 at 256.
 GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N, bool bf16_out) {
   struct Shape {
     int bn;
     double stage, epilogue;
   };
-  static const Shape input[5] = {{256, 0.36, 2.0}, {192, 0.325, 1.6}, {128, 0.22, 1.2}, {64, 0.21, 0.8}, {32, 0.21, 0.6}};
+  static const Shape input[5] = {{256, 0.375, 2.0}, {192, 0.325, 1.6}, {128, 0.22, 1.2}, {64, 0.21, 0.8}, {32, 0.21, 0.6}};
   static const Shape weight32[3] = {{256, 0.74, 4.0}, {192, 0.63, 3.2}, {128, 0.49, 2.2}};
   static const Shape weight16[3] = {{256, 0.45, 2.8}, {192, 0.43, 2.4}, {128, 0.40, 1.6}};
+  constexpr unsigned P = kGradPlanPairs;
   GradPlan g = {};
   const int64_t R = kind == bl::kGradInput ? M : N, L = kind == bl::kGradInput ? N : M;
-  const int64_t kt = (K + 2 * bl::kGtK - 1) / (2 * bl::kGtK);
-  const Shape* shapes = kind == bl::kGradInput ? input : bf16_out ? weight16 : weight32;
   // (32-bit counts: R and L are below 2^31; this runs twice a call)
-  const unsigned r32 = static_cast<unsigned>(R), l32 = static_cast<unsigned>(L), kt32 = static_cast<unsigned>(kt);
-  const double part_us = static_cast<double>(R) * static_cast<double>(K) * 1e-6;
+  const unsigned r32 = static_cast<unsigned>(R), l32 = static_cast<unsigned>(L);
+  const unsigned kt = static_cast<unsigned>((K + 2 * bl::kGtK - 1) / (2 * bl::kGtK));
+  const Shape* shapes = kind == bl::kGradInput ? input : bf16_out ? weight16 : weight32;
+  const double part_us = static_cast<double>(R) * static_cast<double>(K) * 1e-6;   // one part written and read, 8 TB/s
   double best = 1e300;
   for (int b = 0; b < (kind == bl::kGradInput ? 5 : 3); ++b) {
     const unsigned bn = shapes[b].bn, bc = bl::gt_bc(kind, shapes[b].bn);
-    const unsigned rt = (r32 + bn - 1) / bn, tiles = kt32 * rt, nk = (l32 + bc - 1) / bc;
-    const double stage = shapes[b].stage * (bc / 64);
-    const unsigned fill = tiles < kGradPlanPairs ? kGradPlanPairs / tiles : 1u, most = nk / 2 > 1 ? nk / 2 : 1u;
-    const unsigned tries[6] = {1, 2, 3, 4, fill, 2 * fill};
-    for (int j = 0; j < (tiles > 4 * kGradPlanPairs ? 1 : 6); ++j) {
-      if (j > 0 && tries[j] > most && tries[j - 1] >= most) continue;   // the same cut again
-      const unsigned want = tries[j] < most ? tries[j] : most;
+    const unsigned rt = (r32 + bn - 1) / bn, tiles = kt * rt, nk = (l32 + bc - 1) / bc;
+    const double stage = shapes[b].stage * (bc / 64), epi = shapes[b].epilogue;
+    auto consider = [&](unsigned nkv, unsigned per, unsigned chunks, unsigned parts, double t) {
+      if (t >= best) return;
+      best = t;
+      g.bn = static_cast<int>(bn);
+      g.rt = static_cast<int>(rt);
+      g.cut.nkv = static_cast<int>(nkv);
+      g.cut.per = static_cast<int>(per);
+      g.cut.chunks = static_cast<int>(chunks);
+      g.parts = static_cast<int>(parts);
+    };
+    consider(nk, nk, tiles, 1, ((tiles + P - 1) / P) * std::max(nk * stage, epi) + epi);
+    if (tiles > 4 * P || static_cast<uint64_t>(tiles) * (nk + P) >= (1u << 30)) continue;
+    // every tile in the same number of parts, of two stages at least
+    const unsigned fill = tiles < P ? P / tiles : 1u;
+    const unsigned tries[5] = {2, 3, 4, fill, 2 * fill};
+    for (unsigned want : tries) {
+      if (want < 2 || want > nk / 2) continue;
       const unsigned per = (nk + want - 1) / want, splits = (nk + per - 1) / per;
-      const unsigned waves = (tiles * splits + kGradPlanPairs - 1) / kGradPlanPairs;
-      double t = waves * std::max(per * stage, shapes[b].epilogue) + shapes[b].epilogue;
-      if (splits > 1) t += 2.5 + splits * part_us;
-      if (t < best) {
-        best = t;
-        g.bn = static_cast<int>(bn);
-        g.rt = static_cast<int>(rt);
-        g.per = static_cast<int>(per);
-        g.splits = static_cast<int>(splits);
-      }
+      const unsigned waves = (tiles * splits + P - 1) / P;
+      consider(per * splits, per, tiles * splits, splits, waves * std::max(per * stage, epi) + epi + 2.5 + splits * part_us);
+    }
+    // the stages dealt out evenly; a chunk of several pieces has as many epilogues
+    // (and 1.5 us more than parts that end with their tiles)
+    const unsigned per = (tiles * nk + P - 1) / P;
+    if (per >= 2 && per != nk) {
+      const unsigned chunks = (tiles * nk + per - 1) / per, parts = (nk - 1) / per + 2;
+      const double pieces = static_cast<double>(chunks + tiles) / tiles;
+      consider(nk, per, chunks, parts,
+               std::max(per * stage, epi * pieces * tiles / chunks) + epi + 4.0 + pieces * part_us);
     }
   }
   g.kt = static_cast<int>(kt);
   g.ld = static_cast<int64_t>(align_up(static_cast<size_t>(N), 8));
   g.pad_bytes = g.ld == N ? 0 : align_up(static_cast<size_t>(M) * g.ld * 2, 256);
-  g.part_bytes = g.splits > 1 ? static_cast<size_t>(g.splits) * R * K * sizeof(float) : 0;
+  g.part_bytes = g.parts > 1 ? static_cast<size_t>(g.parts) * R * K * sizeof(float) : 0;
   return g;
 }
 
@@ -1710,15 +1727,14 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
   CUtensorMap tmA, tmB, tmD;
   bl::GtArgs P = {};
   P.scale = a.scale;
-  P.gamma = g.splits > 1 ? nullptr : a.gamma;
+  P.gamma = g.parts > 1 ? nullptr : a.gamma;
   P.R = KIND == bl::kGradInput ? a.M : a.N;
   P.L = KIND == bl::kGradInput ? a.N : a.M;
   P.K = a.K;
   P.kt = g.kt;
   P.rt = g.rt;
-  P.splits = g.splits;
-  P.per = g.per;
-  if (g.splits > 1) {
+  P.cut = g.cut;
+  if (g.parts > 1) {
     P.out = parts;
     P.mode = bl::kGtF32;
   } else {
@@ -1740,8 +1756,8 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
     EncodeTiledFn enc = get_encode();
     const bool bf16 = P.mode == bl::kGtTmaBf16;
     const cuuint64_t rs = K * (bf16 ? 2 : 4);
-    const cuuint64_t dims[3] = {K, static_cast<cuuint64_t>(P.R), static_cast<cuuint64_t>(g.splits)};
-    const cuuint64_t strides[2] = {rs, g.splits > 1 ? rs * static_cast<cuuint64_t>(P.R) : rs};
+    const cuuint64_t dims[3] = {K, static_cast<cuuint64_t>(P.R), static_cast<cuuint64_t>(g.parts)};
+    const cuuint64_t strides[2] = {rs, g.parts > 1 ? rs * static_cast<cuuint64_t>(P.R) : rs};
     const cuuint32_t box[3] = {32, bf16 ? static_cast<cuuint32_t>(C::kChunk) : 16, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     if (!enc ||
@@ -1753,8 +1769,7 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
   static std::atomic<int> pairs[kMaxDevices];
   int npairs = max_active_pairs(kern, C::kThreads, C::kSmemBytes, pairs);
   if (npairs <= 0) return BL_ERR_CUDA;
-  const int64_t items = static_cast<int64_t>(g.kt) * g.rt * g.splits;
-  if (npairs > items) npairs = static_cast<int>(items);
+  if (npairs > g.cut.chunks) npairs = g.cut.chunks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * npairs);
   cfg.blockDim = dim3(C::kThreads);
@@ -1807,10 +1822,10 @@ bl_status launch_grad(const bl::GradArgs& a, void* workspace, cudaStream_t strea
       default: st = launch_grad_t<KIND, 2, 256>(a, g, dY, parts, stream); break;
     }
   }
-  if (st != BL_OK || g.splits == 1) return st;
+  if (st != BL_OK || g.parts == 1) return st;
   const size_t n4 = static_cast<size_t>(KIND == bl::kGradInput ? a.M : a.N) * a.K / 4;
   bl::bl_grad_join_kernel<<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, stream>>>(
-      parts, g.splits, n4, a.gamma, a.out, a.out_bf16, a.accumulate);
+      parts, g.cut, g.bn, g.kt, a.K, n4, a.gamma, a.out, a.out_bf16, a.accumulate);
   return last_cuda();
 }
 

@@ -24,8 +24,8 @@
 //     Lanes are k, so a warp's store of one r is 32 neighbouring k.
 // The low-bit matrix is expanded once per tile and never exists in memory as
 // bf16; A's conversion runs beside the MMAs.
-// Few tiles, long sum: the sum is split over pairs; the parts (fp32) meet in
-// bl_grad_join_kernel in a fixed order.
+// Tiles that do not fill the pairs evenly are cut along their sums (GtCut); the
+// parts (fp32) meet in bl_grad_join_kernel in a fixed order.
 // The tensor core truncates when it adds to an fp32 accumulator, so the error
 // of a long sum grows with its length instead of its root: 1.0e-5 of the norm
 // over 4096 tokens, hi + lo included (measured).  An fp32 result is therefore
@@ -109,13 +109,25 @@ struct GtCfg {
   static_assert((3 * kStages + 5) * 8 + 8 <= 512, "barriers");
 };
 
+// How the tiles' sums are cut into the chunks that pairs take: the stages of all
+// tiles in a row, nkv a tile, in chunks of `per`.  per = nkv: whole tiles,
+// written directly.  Otherwise a chunk is a part of a tile or runs from one tile
+// into the next ones; what it has of a tile goes to fp32 part
+// chunk - (the tile's first chunk), and the tile's parts are added in that order.
+// nkv may be above the tile's own stages, so that chunks end with the tile.
+struct GtCut {
+  int nkv, per, chunks;
+  __host__ __device__ int first(int tile) const { return tile * nkv / per; }
+  __host__ __device__ int parts(int tile) const { return ((tile + 1) * nkv - 1) / per - first(tile) + 1; }
+};
+
 struct GtArgs {
   const float* scale;   // [M] (weight)
   const float* gamma;   // device scalar (input), else null
   void* out;            // final output, or fp32 parts [splits][R][K]
   int R, L, K;          // output rows, length of the sum, columns
   int kt, rt;           // tiles along k and r
-  int splits, per;      // parts of the sum, stages a part
+  GtCut cut;
   int mode;             // GtOut
 };
 enum GtOut : int { kGtTmaBf16 = 0, kGtF32 = 1, kGtF32Acc = 2, kGtBf16Acc = 3 };
@@ -298,7 +310,6 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int nk = (P.L + C::kBC - 1) / C::kBC;
-  const int nitems = P.kt * P.rt * P.splits;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -323,14 +334,41 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // an item: tile (k fastest, so neighbouring pairs share a slab of dY) and part of the sum
-  auto item = [&](int it, int& kt, int& rt, int& c0, int& c1, int& part) {
-    const int tile = it % (P.kt * P.rt);
-    part = it / (P.kt * P.rt);
-    kt = tile % P.kt;
-    rt = tile / P.kt;
-    c0 = part * P.per;
-    c1 = min(nk, c0 + P.per);
+  // The pieces of this pair's chunks, in order: tile (k fastest, so that
+  // neighbouring pairs share a slab of dY), stages [c0, c1) and part.  Every role
+  // walks them by itself.
+  struct Walk {
+    int chunk, u, end;          // next stage of the chunk, its end (parts only)
+    int kt, rt, c0, c1, part;
+  };
+  auto start = [&]() {
+    Walk w;
+    w.chunk = pair - npairs;
+    w.u = w.end = 0;
+    return w;
+  };
+  auto next = [&](Walk& w) {
+    if (w.u >= w.end) {
+      w.chunk += npairs;
+      if (w.chunk >= P.cut.chunks) return false;
+      if (P.cut.per != P.cut.nkv) {
+        w.u = w.chunk * P.cut.per;
+        w.end = min(P.kt * P.rt * P.cut.nkv, w.u + P.cut.per);
+      }
+    }
+    int tile = w.chunk;
+    w.c0 = w.part = 0;
+    w.c1 = nk;
+    if (P.cut.per != P.cut.nkv) {
+      tile = w.u / P.cut.nkv;
+      w.c0 = w.u - tile * P.cut.nkv;
+      w.c1 = min(nk, w.c0 + w.end - w.u);
+      w.part = w.chunk - P.cut.first(tile);
+      w.u = min(w.end, (tile + 1) * P.cut.nkv);
+    }
+    w.kt = tile % P.kt;
+    w.rt = tile / P.kt;
+    return true;
   };
 
   if (warp == 0) {
@@ -342,12 +380,10 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     uint32_t g = 0;
     int s = 0;
     bool stop = false;
-    for (int it = pair; it < nitems && !stop; it += npairs) {
-      int kt, rt, c0, c1, part;
-      item(it, kt, rt, c0, c1, part);
-      const int k0 = kt * 2 * kGtK + static_cast<int>(rank) * kGtK;
-      const int r0 = rt * BN + static_cast<int>(rank) * C::kHalf;
-      for (int c = c0; c < c1; ++c, ++g) {
+    for (Walk w = start(); !stop && next(w);) {
+      const int k0 = w.kt * 2 * kGtK + static_cast<int>(rank) * kGtK;
+      const int r0 = w.rt * BN + static_cast<int>(rank) * C::kHalf;
+      for (int c = w.c0; c < w.c1; ++c, ++g) {
         if (g >= static_cast<uint32_t>(S) &&
             !__all_sync(0xffffffffu, mbar_wait(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty))) {
           stop = true;
@@ -387,9 +423,9 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       int s = 0, as = 0, i = 0;
       uint32_t ph = 0;
       bool stop = false, seen = false;
-      for (int it = pair; it < nitems && !stop; it += npairs) {
-        int kt, rt, c0, c1, part;
-        item(it, kt, rt, c0, c1, part);
+      for (Walk w = start(); !stop && next(w);) {
+        int c0 = w.c0;
+        const int c1 = w.c1;
         while (c0 < c1) {   // a segment: the accumulator that was drained longest ago
           const int b = i & 1, ce = min(c1, c0 + min(C::kSegment, c1 - c0));
           // (every decision to give up is taken by the whole warp: elect.sync
@@ -446,10 +482,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     const int ct = threadIdx.x - 64 - grp * 32 * C::kGroupWarps;
     uint32_t g = 0;
     bool stop = false;
-    for (int it = pair; it < nitems && !stop; it += npairs) {
-      int kt, rt, c0, c1, part;
-      item(it, kt, rt, c0, c1, part);
-      for (int c = c0; c < c1; ++c, ++g) {
+    for (Walk w = start(); !stop && next(w);) {
+      for (int c = w.c0; c < w.c1; ++c, ++g) {
         if (g % C::kGroups != static_cast<uint32_t>(grp)) continue;
         const int s = g % S;
         const uint32_t sA = smem_u32(smem) + (g % C::kASlots) * C::kASlotBytes;
@@ -475,14 +509,15 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           // eight different bank groups
           const int row0 = 2 * (ct >> 4) + ((ct >> 2) & 1), gw = (ct & 3) + ((ct >> 3) & 1) * 4;
           constexpr int kRowStep = 32 * C::kGroupWarps / 8;
-          uint32_t w[C::kBC / kRowStep];
+          uint32_t raw4[C::kBC / kRowStep];
 #pragma unroll
-          for (int i = 0; i < C::kBC / kRowStep; ++i) w[i] = ld_shared_u32(raw + (row0 + i * kRowStep) * 32 + gw * 4);
+          for (int i = 0; i < C::kBC / kRowStep; ++i)
+            raw4[i] = ld_shared_u32(raw + (row0 + i * kRowStep) * 32 + gw * 4);
 #pragma unroll
           for (int i = 0; i < C::kBC / kRowStep; ++i) {
             const int row = row0 + i * kRowStep;
             uint32_t v[8];
-            expand16(w[i], v);
+            expand16(raw4[i], v);
             const uint32_t rowa = sA + (gw >> 2) * C::kBlockBytes + row * 128, ch = 2 * (gw & 3), x = row & 7;
             st_shared_v4(rowa + ((ch ^ x) << 4), v[0], v[1], v[2], v[3]);
             st_shared_v4(rowa + (((ch + 1) ^ x) << 4), v[4], v[5], v[6], v[7]);
@@ -537,12 +572,17 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     const float f = P.gamma ? *P.gamma : 1.f;
     uint8_t* so = sOut + (warp - C::kFirstEpi) * C::kOutBytes;
     int i = 0, buf = 0;
-    int kt = 0, rt = 0, c0 = 0, c1 = 0, part = 0;
-    for (int it = pair; it < nitems; ++i) {
-      if (c0 >= c1) item(it, kt, rt, c0, c1, part);
+    Walk w = start();
+    bool fresh = true;   // the piece's first segment
+    for (w.c0 = w.c1 = 0;; ++i) {
+      if (w.c0 >= w.c1) {
+        if (!next(w)) break;
+        fresh = true;
+      }
+      const int part = w.part;
       const int b = i & 1;
-      const int kw = kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32, k = kw + lane;
-      const int r0 = rt * BN + half * C::kHalf;
+      const int kw = w.kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32, k = kw + lane;
+      const int r0 = w.rt * BN + half * C::kHalf;
       const bool kin = kw < P.K;   // K is a multiple of 64: a warp's 32 k are all inside or all outside
       if (P.mode == kGtBf16Acc && kin) {
         // what will be added to, into L2 while the sum is formed
@@ -556,7 +596,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       tc_fence_after();
       // the segments after the first add to what this warp stored itself: those
       // stores have to be complete
-      const bool add = P.mode == kGtF32Acc || (P.mode == kGtF32 && c0 != part * P.per);
+      const bool add = P.mode == kGtF32Acc || (P.mode == kGtF32 && !fresh);
       if (add) {
         if (lane == 0) bulk_wait_group0();
         __syncwarp();
@@ -629,8 +669,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) gt_arrive_leader(&accempty[b]);   // accumulator drained
-      c0 = min(c1, c0 + min(C::kSegment, c1 - c0));
-      if (c0 >= c1) it += npairs;
+      w.c0 += min(C::kSegment, w.c1 - w.c0);
+      fresh = false;
     }
     if (lane == 0) bulk_wait_group0();   // outputs written before exit
   }
@@ -644,15 +684,17 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
   }
 }
 
-// out = f * (sum of the parts, in order) (+ out), four elements a thread.
+// out = f * (sum of a tile's parts, in order) (+ out), four elements a thread.
 __global__ void __launch_bounds__(256)
-    bl_grad_join_kernel(const float* __restrict__ part, int splits, size_t n4, const float* __restrict__ gamma,
-                        void* __restrict__ out, int out_bf16, int accumulate) {
+    bl_grad_join_kernel(const float* __restrict__ part, const GtCut cut, int bn, int kt, int K, size_t n4,
+                        const float* __restrict__ gamma, void* __restrict__ out, int out_bf16, int accumulate) {
   const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n4) return;
+  const int k4 = K / 4, r = static_cast<int>(i / k4), k = 4 * static_cast<int>(i - static_cast<size_t>(r) * k4);
+  const int parts = cut.parts(r / bn * kt + k / (2 * kGtK));
   const float4* p = reinterpret_cast<const float4*>(part);
   float4 s = p[i];
-  for (int j = 1; j < splits; ++j) {
+  for (int j = 1; j < parts; ++j) {
     const float4 t = p[static_cast<size_t>(j) * n4 + i];
     s.x += t.x;
     s.y += t.y;

@@ -498,12 +498,15 @@ def test_binding_refuses():
                             accumulate=True)
 
 
-# One shape for every tile width (32..256 rows of the output) with the sum whole
-# and split, as the cost model chooses them.
-REACH_INPUT = [(33, 64, 1003), (2500, 64, 33), (390, 64, 1500), (2500, 320, 33), (1000, 64, 2050), (1030, 2112, 33),
-               (130, 4160, 4100), (4100, 4160, 33), (4100, 64, 4100)]
-REACH_WEIGHT = [(640, 64, 33), (33, 4160, 520), (2049, 64, 4100), (520, 1088, 3001), (2500, 64, 4100), (770, 64, 33),
-                (4100, 1344, 130), (33, 4160, 3001), (1500, 64, 4100)]
+# One shape for every tile width (32..256 rows of the output) with whole tiles,
+# tiles in equal parts, and stages dealt out to the pairs, as the cost model
+# chooses them.
+REACH_INPUT = [(33, 64, 1003), (33, 64, 6001), (2500, 64, 33), (640, 64, 1500), (6000, 64, 33), (1030, 64, 2050),
+               (640, 1088, 6001), (6000, 320, 33), (130, 2560, 6001), (520, 4160, 6001), (6000, 1088, 33),
+               (2500, 64, 6001), (2049, 2112, 4100)]
+REACH_WEIGHT = [(640, 64, 33), (6000, 64, 33), (33, 320, 6001), (2049, 64, 4100), (6000, 1088, 520),
+                (260, 1088, 6001), (1500, 64, 6001), (6000, 1088, 1003), (770, 64, 33), (1500, 64, 4100),
+                (4100, 2112, 520), (33, 4160, 3001), (2500, 64, 3001), (6000, 576, 2050)]
 
 
 @pytest.mark.parametrize("M,K,N", REACH_INPUT)
