@@ -488,15 +488,19 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         const int s = g % S;
         const uint32_t sA = smem_u32(smem) + (g % C::kASlots) * C::kASlotBytes;
         const uint32_t raw = smem_u32(smem) + C::kInOffset + s * C::kInBytes + C::kBBytes;
-        // the raw rows are here, and the MMAs of the stage that last used the
-        // operand slot are done
+        // The MMAs of the stage that last used the operand slot are done, and the
+        // raw rows are here.  In this order: a parity tells a phase only from its
+        // neighbours, and full[s]'s phase before this one belongs to another group's
+        // stage, g - S, whose rows may land after those this group has just
+        // expanded.  Once stage g - kASlots is through the MMAs, so is that one.
         auto wait_stage = [&]() {
-          bool ok = mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull);
-          // (with no more stages than slots the producer has waited for that)
-          if (C::kASlots < S && ok && g >= static_cast<uint32_t>(C::kASlots)) {
+          static_assert(C::kGroups <= C::kASlots && C::kASlots < S, "phases waited for are one ahead at most");
+          bool ok = true;
+          if (g >= static_cast<uint32_t>(C::kASlots)) {
             const uint32_t gp = g - C::kASlots;
             ok = mbar_wait(&done[gp % S], (gp / S) & 1, abort_flag, limit_ns, kSiteExpEmpty);
           }
+          ok = ok && mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull);
           return __all_sync(0xffffffffu, ok) != 0;
         };
         if constexpr (KIND == kGradInput) {

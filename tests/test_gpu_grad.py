@@ -697,3 +697,73 @@ def test_a_step_behind_a_norm_with_parameters(norm):
     em = 2.0**-24 * (M + 16)
     assert worst(dw, (dy * xh).sum(0), em * (dy * xh).abs().sum(0) + 1e-300) <= 1.0
     assert (db is not None) == la and (db is None or worst(db, dy.sum(0), em * dy.abs().sum(0) + 1e-300) <= 1.0)
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 1024, 4096), (16, 2560, 6912), (192, 2048, 4100), (256, 2048, 8192),
+                                   (260, 4160, 9001), (320, 8192, 8192), (256, 8192, 28672)])
+def test_accumulating_over_many_tiles(M, K, N):
+    # many tiles a pair with few stages each: the epilogue, with loads and stores
+    # of the whole output, is what the others wait for
+    g = torch.Generator(device="cuda").manual_seed(M)
+    q = torch.randint(-127, 128, (M, K), generator=g, device="cuda").to(torch.int8)
+    s = torch.rand(M, generator=g, device="cuda") + 1
+    dY = (torch.randn(M, N, generator=g, device="cuda") * 1e-3).to(torch.bfloat16)
+    for dtype in (torch.float32, torch.bfloat16):
+        plain = bl.bl_backward_weight(dY, q, s, out=torch.empty(N, K, dtype=dtype, device="cuda"))
+        base = (torch.randn(N, K, generator=g, device="cuda") * 1e-2).to(dtype)
+        out = base.clone()
+        bl.bl_backward_weight(dY, q, s, out=out, accumulate=True)
+        for a in (0, N // 2, N - 24):
+            b = slice(a, a + 24)
+            check_dw(plain[b], dY[:, b], q, s)
+            check_dw(out[b], dY[:, b], q, s, base=base[b])
+        if dtype == torch.float32:   # one rounding, of the same sum
+            assert torch.equal(out, base + plain)
+        out.zero_()
+        for _ in range(3):
+            bl.bl_backward_weight(dY, q, s, out=out.zero_(), accumulate=True)
+        assert torch.equal(out, plain)
+
+
+@pytest.mark.parametrize("M,K,N", [(10240, 2048, 1280), (6200, 1088, 1400), (4500, 2112, 4100)])
+def test_several_accumulators_a_tile(M, K, N):
+    # sums longer than one accumulator takes, whole and in parts
+    *_, q, s = layer(M, K, N, 1)
+    dY = grads(M, N, 2)
+    base = (torch.randn(N, K, generator=torch.Generator().manual_seed(3)) * 1e-2).cuda()
+    for acc in (False, True):
+        runs = []
+        for _ in range(2):
+            dW = Guarded((N, K), torch.float32)
+            dW.t.copy_(base)
+            bl.bl_backward_weight(dY, q, s, out=dW.t, accumulate=acc)
+            assert dW.intact()
+            runs.append(dW.t.clone())
+        assert torch.equal(runs[0], runs[1])
+        check_dw(runs[0], dY, q, s, base=base if acc else None)
+
+
+def test_runs_repeat_bit_for_bit():
+    # long rings of stages whose loads may land out of order; a stage expanded
+    # from rows that are not its own shows in some runs only
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for M, K, N in ((10240, 2048, 1280), (4500, 2112, 4100), (4096, 512, 2048)):
+        q = torch.randint(-127, 128, (M, K), generator=g, device="cuda").to(torch.int8)
+        s = torch.rand(M, generator=g, device="cuda") + 1
+        dY = (torch.randn(M, N, generator=g, device="cuda") * 1e-3).to(torch.bfloat16)
+        for dtype in (torch.float32, torch.bfloat16):
+            first = bl.bl_backward_weight(dY, q, s, dtype)
+            check_dw(first, dY, q, s)
+            out = torch.empty_like(first)
+            for _ in range(60):
+                assert torch.equal(bl.bl_backward_weight(dY, q, s, out=out), first)
+    for M, K, N in ((4096, 2048, 6912), (400, 2112, 9000), (128, 2560, 20000), (33, 1088, 20000), (17, 1088, 9000)):
+        Wp = torch.randint(0, 256, (N, K // 4), generator=g, device="cuda").to(torch.uint8)
+        Wp = torch.where((Wp & (Wp >> 1) & 0x55) != 0, Wp & 0x55, Wp)   # no field is 3
+        gamma = torch.full((1,), 0.02, device="cuda")
+        dY = (torch.randn(M, N, generator=g, device="cuda") * 1e-3).to(torch.bfloat16)
+        first = bl.bl_backward_input(dY, Wp, gamma, K)
+        check_dx(first, dY, bl.bl_unpack_weights(Wp, N, K).to(F64), gamma)
+        out = torch.empty_like(first)
+        for _ in range(60):
+            assert torch.equal(bl.bl_backward_input(dY, Wp, gamma, K, out=out), first)
