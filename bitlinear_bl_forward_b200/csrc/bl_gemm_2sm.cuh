@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     tmem_relinquish_pair();
   }
   tc_fence_before();
+  __syncwarp();   // thread 0 comes last, and the barrier is a warp's instruction
   cluster_sync_all();   // barriers of both CTAs initialised before any remote arrive
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -364,6 +365,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
 #pragma unroll 1
       for (int c0 = col0; c0 < col0 + kQEpiCols; c0 += 32) {
         uint32_t v[32];
+        __syncwarp();   // (lanes with n >= N are ahead, and tcgen05.ld is a warp's instruction)
         tmem_ld_32x32b_x32(tmem + lane_base + b * kQAccCols + c0, v);
         tmem_wait_ld();
         if (n < N) {

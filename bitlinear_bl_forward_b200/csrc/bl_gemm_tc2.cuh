@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(P2Warps<EXPG>::kThreads, 1)
 #pragma unroll 1
       for (int c0 = 0; c0 < BN; c0 += kChunk) {
         uint32_t v[32];
+        __syncwarp();   // (lanes with n >= N are ahead, and tcgen05.ld is a warp's instruction)
         if constexpr (kChunk == 32)
           tmem_ld_32x32b_x32(tmem + lane_base + b * C::kAccCols + c0, v);
         else

@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     tmem_relinquish_pair();
   }
   tc_fence_before();
+  __syncwarp();   // thread 0 comes last, and the barrier is a warp's instruction
   cluster_sync_all();   // barriers of both CTAs initialised before any remote arrive
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -608,6 +609,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < C::kHalf; c += C::kChunk) {
         uint32_t v[32];
+        __syncwarp();   // tcgen05.ld is a warp's instruction, and lane 0 may still be issuing the last store
         if (C::kChunk == 32)
           tmem_ld_32x32b_x32(tmem + lane_base + b * BN + half * C::kHalf + c, v);
         else
