@@ -1739,7 +1739,7 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
     P.mode = bl::kGtF32;
   } else {
     P.out = a.out;
-    P.mode = !a.out_bf16 ? (a.accumulate ? bl::kGtF32Acc : bl::kGtF32) : (a.accumulate ? bl::kGtBf16Acc : bl::kGtTmaBf16);
+    P.mode = !a.out_bf16 ? (a.accumulate ? bl::kGtF32Acc : bl::kGtF32) : (a.accumulate ? bl::kGtBf16Acc : bl::kGtBf16);
   }
   const bool ok =
       (KIND == bl::kGradInput ? encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, N, K / 4, K / 4, C::kBC,
@@ -1750,22 +1750,18 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
                 KIND == bl::kGradInput ? C::kHalf : C::kBC, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return BL_ERR_CUDA;
   // output tiles: [parts][R][K] (a tile that ends past R is clipped there)
-  if (P.mode == bl::kGtBf16Acc) {
-    tmD = tmB;   // not used
-  } else {
-    EncodeTiledFn enc = get_encode();
-    const bool bf16 = P.mode == bl::kGtTmaBf16;
-    const cuuint64_t rs = K * (bf16 ? 2 : 4);
-    const cuuint64_t dims[3] = {K, static_cast<cuuint64_t>(P.R), static_cast<cuuint64_t>(g.parts)};
-    const cuuint64_t strides[2] = {rs, g.parts > 1 ? rs * static_cast<cuuint64_t>(P.R) : rs};
-    const cuuint32_t box[3] = {32, bf16 ? static_cast<cuuint32_t>(C::kChunk) : 16, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    if (!enc ||
-        enc(&tmD, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, P.out, dims, strides,
-            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return BL_ERR_CUDA;
-  }
+  EncodeTiledFn enc = get_encode();
+  const bool bf16 = P.mode == bl::kGtBf16 || P.mode == bl::kGtBf16Acc;
+  const cuuint64_t rs = K * (bf16 ? 2 : 4);
+  const cuuint64_t dims[3] = {K, static_cast<cuuint64_t>(P.R), static_cast<cuuint64_t>(g.parts)};
+  const cuuint64_t strides[2] = {rs, g.parts > 1 ? rs * static_cast<cuuint64_t>(P.R) : rs};
+  const cuuint32_t box[3] = {32, bf16 ? static_cast<cuuint32_t>(C::kChunk) : 16, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (!enc ||
+      enc(&tmD, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, P.out, dims, strides,
+          box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return BL_ERR_CUDA;
   static std::atomic<int> pairs[kMaxDevices];
   int npairs = max_active_pairs(kern, C::kThreads, C::kSmemBytes, pairs);
   if (npairs <= 0) return BL_ERR_CUDA;

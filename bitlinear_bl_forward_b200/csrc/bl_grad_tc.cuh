@@ -130,7 +130,7 @@ struct GtArgs {
   GtCut cut;
   int mode;             // GtOut
 };
-enum GtOut : int { kGtTmaBf16 = 0, kGtF32 = 1, kGtF32Acc = 2, kGtBf16Acc = 3 };
+enum GtOut : int { kGtBf16 = 0, kGtF32 = 1, kGtF32Acc = 2, kGtBf16Acc = 3 };
 
 // Instruction descriptor: kind::f16, bf16 x bf16 -> f32; A MN-major, B
 // MN-major or K-major.
@@ -569,13 +569,19 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
   } else {
     // ---------------- epilogue (both CTAs) ----------------
     // A warp has 32 k (its lanes) of half of the tile's r.  Results leave through
-    // staging tiles and TMA: stores, or reductions that add
-    // to fp32 in memory (plain stores of 128 bytes a warp took 7100 clocks a tile,
-    // the adds 8600).  A bf16 result that is added to is read and rounded once.
+    // staging tiles and TMA: stores, or reductions that add to fp32 in memory (plain
+    // stores of 128 bytes a warp took 7100 clocks a tile).  A bf16 result that is
+    // added to is rounded once: what is there comes into the staging tile 16 bytes a
+    // lane, and each lane adds its column.  Output of 8192 x 28672, 16 tokens: fp32 153
+    // us stored, 403 added to (4.7 TB/s; 540 with plain loads instead of reductions);
+    // bf16 128 and 274 us (930 with plain loads and stores of 2 bytes a lane).
     const int q = warp & 3, half = (warp - C::kFirstEpi) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float f = P.gamma ? *P.gamma : 1.f;
     uint8_t* so = sOut + (warp - C::kFirstEpi) * C::kOutBytes;
+    // (two terms: an fp32 result; one: a bf16 one, or fp32 parts of it)
+    const bool bf16 = TERMS == 1 && (P.mode == kGtBf16 || P.mode == kGtBf16Acc);
+    const bool bf16_acc = KIND == kGradWeight && TERMS == 1 && P.mode == kGtBf16Acc;
     int i = 0, buf = 0;
     Walk w = start();
     bool fresh = true;   // the piece's first segment
@@ -586,10 +592,10 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       }
       const int part = w.part;
       const int b = i & 1;
-      const int kw = w.kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32, k = kw + lane;
+      const int kw = w.kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32;
       const int r0 = w.rt * BN + half * C::kHalf;
       const bool kin = kw < P.K;   // K is a multiple of 64: a warp's 32 k are all inside or all outside
-      if (P.mode == kGtBf16Acc && kin) {
+      if (bf16_acc && kin) {
         // what will be added to, into L2 while the sum is formed
         for (int t = lane; t < C::kHalf && r0 + t < P.R; t += 32)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t*>(P.out) +
@@ -601,7 +607,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       tc_fence_after();
       // the segments after the first add to what this warp stored itself: those
       // stores have to be complete
-      const bool add = P.mode == kGtF32Acc || (P.mode == kGtF32 && !fresh);
+      const bool add = TERMS == 2 && (P.mode == kGtF32Acc || !fresh);
       if (add) {
         if (lane == 0) bulk_wait_group0();
         __syncwarp();
@@ -617,58 +623,63 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         tmem_wait_ld();
         const int r = r0 + c;
         if (!kin || r >= P.R) continue;
-        if (P.mode != kGtBf16Acc) {
-          if (P.mode == kGtTmaBf16) {
-            if (lane == 0) bulk_wait_group_read0();   // the last store has read the tile
+        if (bf16) {
+          if (lane == 0) bulk_wait_group_read0();   // the last store has read the tile
+          __syncwarp();
+          if (bf16_acc) {
+            // rows (lane / 4) + 8 j of the chunk, 8 columns a lane
+            const uint16_t* y = static_cast<const uint16_t*>(P.out) + static_cast<size_t>(r) * P.K + kw + (lane & 3) * 8;
+            const uint32_t dst = smem_u32(so) + lane * 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int rr = (lane >> 2) + 8 * j;
+              if (r + rr < P.R)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * j),
+                             "l"(y + static_cast<size_t>(rr) * P.K)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
 #pragma unroll
             for (int t = 0; t < C::kChunk; ++t)
-              reinterpret_cast<uint16_t*>(so)[t * 32 + lane] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[t]) * f));
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&tmD, kw, r, part, so);
-              bulk_commit_group();
-            }
-            continue;
+              v[t] = __float_as_uint(
+                  __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(so)[t * 32 + lane]) << 16) +
+                  __uint_as_float(v[t]));
           }
 #pragma unroll
-          for (int h = 0; h < C::kChunk; h += 16) {
-            if (r + h >= P.R) break;
-            uint8_t* tile = so + (TERMS == 2 ? buf * 2048 : 0);   // two tiles in turn, or one
-            buf ^= 1;
-            if (lane == 0) {
-              if (TERMS == 2)
-                bulk_wait_group_read1();
-              else
-                bulk_wait_group_read0();
-            }
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < 16; ++t) reinterpret_cast<uint32_t*>(tile)[t * 32 + lane] = v[h + t];
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (add)
-                tma_reduce_add_3d(&tmD, kw, r + h, part, tile);
-              else
-                tma_store_3d(&tmD, kw, r + h, part, tile);
-              bulk_commit_group();
-            }
+          for (int t = 0; t < C::kChunk; ++t)
+            reinterpret_cast<uint16_t*>(so)[t * 32 + lane] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[t]) * f));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmD, kw, r, part, so);
+            bulk_commit_group();
           }
-        } else {
-          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.out) + static_cast<size_t>(r) * P.K + k;
-          const int n = min(C::kChunk, P.R - r);
-          const uint32_t ld = static_cast<uint32_t>(P.K);
+          continue;
+        }
 #pragma unroll
-          for (int h = 0; h < C::kChunk; h += 16) {
-            float old[16];
+        for (int h = 0; h < C::kChunk; h += 16) {
+          if (r + h >= P.R) break;
+          uint8_t* tile = so + (TERMS == 2 ? buf * 2048 : 0);   // two tiles in turn, or one
+          buf ^= 1;
+          if (lane == 0) {
+            if (TERMS == 2)
+              bulk_wait_group_read1();
+            else
+              bulk_wait_group_read0();
+          }
+          __syncwarp();
 #pragma unroll
-            for (int t = 0; t < 16; ++t) old[t] = h + t < n ? __bfloat162float(y[(h + t) * ld]) : 0.f;
-#pragma unroll
-            for (int t = 0; t < 16; ++t)
-              if (h + t < n) y[(h + t) * ld] = __float2bfloat16_rn(old[t] + __uint_as_float(v[h + t]));
+          for (int t = 0; t < 16; ++t) reinterpret_cast<uint32_t*>(tile)[t * 32 + lane] = v[h + t];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (add)
+              tma_reduce_add_3d(&tmD, kw, r + h, part, tile);
+            else
+              tma_store_3d(&tmD, kw, r + h, part, tile);
+            bulk_commit_group();
           }
         }
       }
