@@ -1625,6 +1625,7 @@ struct GradPlan {
   int kt, rt;            // tiles along k and r
   bl::GtCut cut;         // chunks of the tiles' sums
   int parts;             // most parts of a tile (1: written directly)
+  int part_row;          // first output row with parts
   int64_t ld;            // row stride of dY in elements (N, or a padded copy's)
   size_t pad_bytes, part_bytes;
 };
@@ -1632,18 +1633,19 @@ struct GradPlan {
 constexpr unsigned kGradPlanPairs = 74;   // CTA pairs of a B200
 
 // Tiles of 256 k by bn r on 74 CTA pairs, and how their sums are cut: whole
-// tiles, every tile in the same number of parts, or the stages of all tiles dealt
-// out evenly to the pairs.  Whichever takes least by this model of the kernel, in
-// us:
+// tiles; every tile in the same number of parts; or whole waves of whole tiles and
+// the stages of the remaining tiles dealt out evenly to the pairs.  Whichever takes
+// least by this model of the kernel, in us:
 //   * 64 rows of the sum take `stage`, about the same for every bn up to 128
 //     (there the expanded operand's way through shared memory is the limit);
 //   * pairs work in waves of chunks; a wave is as long as its sums, or as its
 //     epilogues where those are longer (few rows);
 //   * parts are written and read once more, and need a second launch.
-// Both sides measured: the 2B down projection's input gradient at bn = 256
-// takes 91 us; the up projection's (4096 x 2560 out) 105 us at 192 (three waves)
-// where 256 needs three of its longer ones (150, before the last steps); 300
-// tokens take 20 us at 128 in two parts, 26 in one, 38 at 256.
+// Both sides measured: 300 tokens take 20 us at 128 in two parts, 26 in one, 38 at
+// 256; 4096 tokens of the 2B up projection's input gradient (160 tiles at 256) 125 us
+// with 12 tiles dealt out, 143 as 220 whole tiles of 192; 8192 tokens of a 4096 x 4096
+// layer (256 tiles) 384 and 240 us (fp32, bf16 weight gradient) with 34 tiles dealt
+// out, 419 and 279 with all; the 2B up projection's weight gradient 188 us either way.
 GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N, bool bf16_out) {
   struct Shape {
     int bn;
@@ -1665,41 +1667,50 @@ GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N, bool bf16_out) {
     const unsigned bn = shapes[b].bn, bc = bl::gt_bc(kind, shapes[b].bn);
     const unsigned rt = (r32 + bn - 1) / bn, tiles = kt * rt, nk = (l32 + bc - 1) / bc;
     const double stage = shapes[b].stage * (bc / 64), epi = shapes[b].epilogue;
-    auto consider = [&](unsigned nkv, unsigned per, unsigned chunks, unsigned parts, double t) {
+    auto consider = [&](unsigned whole, unsigned nkv, unsigned per, unsigned chunks, unsigned parts, double t) {
       if (t >= best) return;
       best = t;
       g.bn = static_cast<int>(bn);
       g.rt = static_cast<int>(rt);
+      g.cut.whole = static_cast<int>(whole);
       g.cut.nkv = static_cast<int>(nkv);
       g.cut.per = static_cast<int>(per);
       g.cut.chunks = static_cast<int>(chunks);
       g.parts = static_cast<int>(parts);
     };
-    consider(nk, nk, tiles, 1, ((tiles + P - 1) / P) * std::max(nk * stage, epi) + epi);
-    if (tiles > 4 * P || static_cast<uint64_t>(tiles) * (nk + P) >= (1u << 30)) continue;
+    consider(tiles, nk, nk, tiles, 1, ((tiles + P - 1) / P) * std::max(nk * stage, epi) + epi);
     // every tile in the same number of parts, of two stages at least
-    const unsigned fill = tiles < P ? P / tiles : 1u;
-    const unsigned tries[5] = {2, 3, 4, fill, 2 * fill};
-    for (unsigned want : tries) {
-      if (want < 2 || want > nk / 2) continue;
-      const unsigned per = (nk + want - 1) / want, splits = (nk + per - 1) / per;
-      const unsigned waves = (tiles * splits + P - 1) / P;
-      consider(per * splits, per, tiles * splits, splits, waves * std::max(per * stage, epi) + epi + 2.5 + splits * part_us);
+    if (tiles <= 4 * P && static_cast<uint64_t>(tiles) * (nk + P) < (1u << 30)) {
+      const unsigned fill = tiles < P ? P / tiles : 1u;
+      const unsigned tries[5] = {2, 3, 4, fill, 2 * fill};
+      for (unsigned want : tries) {
+        if (want < 2 || want > nk / 2) continue;
+        const unsigned per = (nk + want - 1) / want, splits = (nk + per - 1) / per;
+        const unsigned waves = (tiles * splits + P - 1) / P;
+        consider(0, per * splits, per, tiles * splits, splits,
+                 waves * std::max(per * stage, epi) + epi + 2.5 + splits * part_us);
+      }
     }
-    // the stages dealt out evenly; a chunk of several pieces has as many epilogues
-    // (and 1.5 us more than parts that end with their tiles)
-    const unsigned per = (tiles * nk + P - 1) / P;
-    if (per >= 2 && per != nk) {
-      const unsigned chunks = (tiles * nk + per - 1) / per, parts = (nk - 1) / per + 2;
-      const double pieces = static_cast<double>(chunks + tiles) / tiles;
-      consider(nk, per, chunks, parts,
-               std::max(per * stage, epi * pieces * tiles / chunks) + epi + 4.0 + pieces * part_us);
+    // whole waves of whole tiles, and the stages of the other tiles dealt out evenly;
+    // a chunk of several pieces has as many epilogues (and 1.5 us more than parts that
+    // end with their tiles)
+    const unsigned whole = tiles / P * P, rest = tiles - whole;
+    if (rest > 0 && static_cast<uint64_t>(rest) * nk < (1u << 30)) {
+      const unsigned per = (rest * nk + P - 1) / P;
+      if (per >= 2 && per != nk) {
+        const unsigned chunks = (rest * nk + per - 1) / per, parts = (nk - 1) / per + 2;
+        const double pieces = static_cast<double>(chunks + rest) / rest;
+        consider(whole, nk, per, whole + chunks, parts,
+                 whole / P * std::max(nk * stage, epi) + std::max(per * stage, epi * pieces * rest / chunks) + epi + 4.0 +
+                     (whole ? 0.5 * parts : 0.0) + pieces * part_us * rest / tiles);
+      }
     }
   }
   g.kt = static_cast<int>(kt);
   g.ld = static_cast<int64_t>(align_up(static_cast<size_t>(N), 8));
   g.pad_bytes = g.ld == N ? 0 : align_up(static_cast<size_t>(M) * g.ld * 2, 256);
-  g.part_bytes = g.parts > 1 ? static_cast<size_t>(g.parts) * R * K * sizeof(float) : 0;
+  g.part_row = g.cut.whole / static_cast<int>(kt) * g.bn;
+  g.part_bytes = g.parts > 1 ? static_cast<size_t>(g.parts) * (R - g.part_row) * K * sizeof(float) : 0;
   return g;
 }
 
@@ -1724,23 +1735,19 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kern, C::kSmemBytes, &done)) return BL_ERR_CUDA;
   const uint64_t M = a.M, K = a.K, N = a.N;
-  CUtensorMap tmA, tmB, tmD;
+  CUtensorMap tmA, tmB, tmD, tmP;
   bl::GtArgs P = {};
   P.scale = a.scale;
-  P.gamma = g.parts > 1 ? nullptr : a.gamma;
+  P.gamma = a.gamma;
   P.R = KIND == bl::kGradInput ? a.M : a.N;
   P.L = KIND == bl::kGradInput ? a.N : a.M;
   P.K = a.K;
   P.kt = g.kt;
   P.rt = g.rt;
   P.cut = g.cut;
-  if (g.parts > 1) {
-    P.out = parts;
-    P.mode = bl::kGtF32;
-  } else {
-    P.out = a.out;
-    P.mode = !a.out_bf16 ? (a.accumulate ? bl::kGtF32Acc : bl::kGtF32) : (a.accumulate ? bl::kGtBf16Acc : bl::kGtBf16);
-  }
+  P.out = a.out;
+  P.part_row = g.part_row;
+  P.accumulate = a.accumulate;
   const bool ok =
       (KIND == bl::kGradInput ? encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, N, K / 4, K / 4, C::kBC,
                                           bl::kGtK / 4, CU_TENSOR_MAP_SWIZZLE_NONE)
@@ -1749,19 +1756,21 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
       encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, M, N, static_cast<uint64_t>(g.ld) * 2,
                 KIND == bl::kGradInput ? C::kHalf : C::kBC, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return BL_ERR_CUDA;
-  // output tiles: [parts][R][K] (a tile that ends past R is clipped there)
-  EncodeTiledFn enc = get_encode();
-  const bool bf16 = P.mode == bl::kGtBf16 || P.mode == bl::kGtBf16Acc;
-  const cuuint64_t rs = K * (bf16 ? 2 : 4);
-  const cuuint64_t dims[3] = {K, static_cast<cuuint64_t>(P.R), static_cast<cuuint64_t>(g.parts)};
-  const cuuint64_t strides[2] = {rs, g.parts > 1 ? rs * static_cast<cuuint64_t>(P.R) : rs};
-  const cuuint32_t box[3] = {32, bf16 ? static_cast<cuuint32_t>(C::kChunk) : 16, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  if (!enc ||
-      enc(&tmD, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, P.out, dims, strides,
-          box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return BL_ERR_CUDA;
+  // output tiles, clipped at the last row: of the result, and of the fp32 parts
+  auto encode_out = [&](CUtensorMap* tm, void* base, bool bf16, cuuint64_t rows, cuuint64_t planes) {
+    EncodeTiledFn enc = get_encode();
+    const cuuint64_t rs = K * (bf16 ? 2 : 4);
+    const cuuint64_t dims[3] = {K, rows, planes};
+    const cuuint64_t strides[2] = {rs, rs * rows};
+    const cuuint32_t box[3] = {32, bf16 ? static_cast<cuuint32_t>(C::kChunk) : 16, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc && enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims,
+                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!encode_out(&tmD, a.out, a.out_bf16 != 0, P.R, 1)) return BL_ERR_CUDA;
+  tmP = tmD;   // not used without parts
+  if (g.parts > 1 && !encode_out(&tmP, parts, false, P.R - g.part_row, g.parts)) return BL_ERR_CUDA;
   static std::atomic<int> pairs[kMaxDevices];
   int npairs = max_active_pairs(kern, C::kThreads, C::kSmemBytes, pairs);
   if (npairs <= 0) return BL_ERR_CUDA;
@@ -1779,7 +1788,7 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const unsigned long long lim = kWaitLimitNs;
-  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, P, lim) != cudaSuccess) return BL_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, tmP, P, lim) != cudaSuccess) return BL_ERR_CUDA;
   return last_cuda();
 }
 
@@ -1819,9 +1828,19 @@ bl_status launch_grad(const bl::GradArgs& a, void* workspace, cudaStream_t strea
     }
   }
   if (st != BL_OK || g.parts == 1) return st;
-  const size_t n4 = static_cast<size_t>(KIND == bl::kGradInput ? a.M : a.N) * a.K / 4;
-  bl::bl_grad_join_kernel<<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, stream>>>(
-      parts, g.cut, g.bn, g.kt, a.K, n4, a.gamma, a.out, a.out_bf16, a.accumulate);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((g.kt * g.rt - g.cut.whole) * (g.bn / bl::kGtJoinRows));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, bl::bl_grad_join_kernel, static_cast<const float*>(parts), g.cut, g.bn, g.kt,
+                         KIND == bl::kGradInput ? a.M : a.N, a.K, g.part_row, a.gamma, a.out, a.out_bf16,
+                         a.accumulate) != cudaSuccess)
+    return BL_ERR_CUDA;
   return last_cuda();
 }
 
