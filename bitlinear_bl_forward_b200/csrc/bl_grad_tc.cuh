@@ -24,8 +24,8 @@
 //     Lanes are k, so a warp's store of one r is 32 neighbouring k.
 // The low-bit matrix is expanded once per tile and never exists in memory as
 // bf16; A's conversion runs beside the MMAs.
-// Tiles that do not fill the pairs evenly are cut along their sums (GtCut); the
-// parts (fp32) meet in bl_grad_join_kernel in a fixed order.
+// Tiles behind the last whole wave are cut along their sums (GtCut); the parts
+// (fp32) meet in bl_grad_join_kernel in a fixed order.
 // The tensor core truncates when it adds to an fp32 accumulator, so the error
 // of a long sum grows with its length instead of its root: 1.0e-5 of the norm
 // over 4096 tokens, hi + lo included (measured).  An fp32 result is therefore
@@ -41,11 +41,11 @@
 // input gradient, 640 for a bf16 and 1000 (of 1024) for an fp32 weight gradient.
 // At BN <= 128 A's way through shared memory alone is 256 of them for 256 clocks of
 // tensor work or less.  Measured (B200): 2B down projection, M = 4096, 91 us alone
-// (1.59 PFLOP/s, the tensor pipe 83% active), 110 us in a seconds-long run under
-// the power cap (1.31); 2B up projection's fp32 gradient 190 and 225 us (twice
-// 0.76 PFLOP/s; pipe 92% active while a pair works, four waves for 3.65);
-// 4-bit-activation layer's bf16 gradient 142 and 158 us (1.30; pipe 74%); 70B-class
-// layer with 128 tokens 57 us (1.05; pipe 61%, DRAM 14%).
+// (1.59 PFLOP/s, the tensor pipe 84% active), 109 us in a seconds-long run under
+// the power cap (1.33); 2B up projection's fp32 gradient 188 and 222 us (twice
+// 0.77 PFLOP/s; pipe 92% active while a pair works); 4-bit-activation layer's bf16
+// gradient 131 and 155 us (1.41; pipe 75%); 70B-class layer with 128 tokens 52 us and
+// 5 for the join (1.06; pipe 58%).
 #pragma once
 
 #include <cuda_bf16.h>

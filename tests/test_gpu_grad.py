@@ -767,3 +767,15 @@ def test_runs_repeat_bit_for_bit():
         out = torch.empty_like(first)
         for _ in range(60):
             assert torch.equal(bl.bl_backward_input(dY, Wp, gamma, K, out=out), first)
+
+
+# a full wave of whole tiles and a few more, whose stages are dealt out: their first
+# row of tiles is whole in part, the last tiles end past K and past the last row
+REACH_REST = [(1030, 4160, 4100), (4100, 1088, 4100), (2049, 2112, 2050), (2500, 2112, 2050), (2500, 1088, 4100)]
+
+
+@pytest.mark.parametrize("M,K,N", REACH_REST)
+def test_tiles_behind_whole_waves(M, K, N):
+    test_backward_input_tiles(M, K, N)
+    test_backward_weight_tiles(M, K, N, torch.float32)
+    test_backward_weight_tiles(M, K, N, torch.bfloat16)
