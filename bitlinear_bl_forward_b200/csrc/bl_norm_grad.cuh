@@ -16,11 +16,13 @@
 // result does not depend on the run).
 //
 // Bound by the bytes: one read of every input row and one write of every output
-// row.  Measured (B200, 4096 x 2560, rows in HBM): forward 7.4 us, 5.7 TB/s (87%
+// row.  Measured (B200, 4096 x 2560, rows in HBM): forward 7.1 us, 5.9 TB/s (90%
 // of a copy's rate); row gradients alone 10.1 us; with the weight's gradient 13
-// (RMSNorm) to 16 us (LayerNorm) and 3 us for the join, against 9.6 us of bytes:
-// there the instructions for the column sums fill half of the issue slots and the
-// barrier of a step the rest.
+// (RMSNorm) to 16 us (LayerNorm) and 4 us for the join, against 9.6 us of bytes.
+// There a group has seven steps, and what comes on top is the first fetch, the merge
+// of the groups and the partial rows: neither fewer instructions a step (rows kept in
+// registers between the passes) nor a hidden barrier (a step's dX behind the next
+// step's sums) made it faster.
 #pragma once
 
 #include "bl_act.cuh"
