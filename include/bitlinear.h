@@ -424,7 +424,8 @@ BL_API bl_status bl_forward_norm_grouped(int count, const bl_linear* problems, i
  * (dW is the gradient of the latent weights W).  What has to be kept between
  * the two passes is M*K bytes of codes and 4*M bytes of scales, half of the
  * bf16 activations, and it is exactly what the forward multiplied.
- * Values of dY that are NaN or Inf give undefined (but memory-safe) results.
+ * A NaN or Inf dY[m,n] makes row m of dX and row n of dW not finite (Inf or NaN),
+ * and changes nothing else.
  * Outputs that overlap an input return BL_ERR_INVALID_ARG, but for the rows that
  * a norm may take in place (exactly the same range).  A workspace is clobbered:
  * calls that may overlap on the GPU (streams, graphs replayed at once) need one

@@ -779,3 +779,24 @@ def test_tiles_behind_whole_waves(M, K, N):
     test_backward_input_tiles(M, K, N)
     test_backward_weight_tiles(M, K, N, torch.float32)
     test_backward_weight_tiles(M, K, N, torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 64, 9), (70, 320, 130), (257, 1344, 1003), (4200, 192, 260)])
+def test_values_that_are_not_finite_stay_in_their_rows(M, K, N):
+    _, Wp, gamma, C, q, s = layer(M, K, N, 1)
+    q[q == 0] = 1   # (Inf times a zero code is NaN; times any other it is not finite)
+    dY = grads(M, N, 2)
+    bad = dY.clone()
+    ms, ns = sorted({0, M // 2, M - 1}), sorted({0, N // 2, N - 1})
+    for i, (m, n) in enumerate(zip(ms, ns)):
+        bad[m, n] = (float("nan"), float("inf"), float("-inf"))[i]
+    ms, ns = ms[:len(ns)], ns[:len(ms)]
+    rest = torch.ones(M, dtype=torch.bool, device="cuda")
+    rest[ms] = False
+    a, b = bl.bl_backward_input(dY, Wp, gamma, K), bl.bl_backward_input(bad, Wp, gamma, K)
+    assert torch.equal(a[rest], b[rest]) and not torch.isfinite(b[ms].float()).any()
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[ns] = False
+    for dtype in (torch.float32, torch.bfloat16):
+        a, b = bl.bl_backward_weight(dY, q, s, dtype), bl.bl_backward_weight(bad, q, s, dtype)
+        assert torch.equal(a[rest], b[rest]) and not torch.isfinite(b[ns].float()).any()
