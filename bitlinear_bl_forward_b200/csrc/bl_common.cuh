@@ -139,10 +139,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank
       : "memory");
 }
 
-// Relaxed variant: for signalling completed tcgen05.st data (the data is in
-// tensor memory once tcgen05.wait::st returns, and tcgen05.fence::before_
-// thread_sync orders it before this arrive); a cluster-scope release here
-// costs about half a microsecond per arrive.
+// Relaxed variant: for hand-overs whose data stays within one SM and is ordered
+// before the arrive by other means: completed tcgen05.st data (in tensor memory
+// once tcgen05.wait::st returns, and tcgen05.fence::before_thread_sync orders it
+// before this arrive), or shared memory behind fence.proxy.async.  A cluster-scope
+// release here costs about half a microsecond per arrive.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"

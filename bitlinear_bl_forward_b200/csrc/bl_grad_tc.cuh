@@ -34,6 +34,20 @@
 // first segment and adds the others to its own output, which is still in L2.
 // Segments of 1024 tokens cost 3% more.
 //
+// Order between the two CTAs.  Waits on barriers that the other CTA's threads or
+// the leader's commits arrive on (ready, done, accfull, accempty) acquire at
+// cluster scope; full is a CTA's own.  Arrivals on the leader's ready and accempty
+// are relaxed at cluster scope, which is enough because no data crosses:
+//   ready     an expanded tile is written, fenced and read in one SM's shared
+//             memory: every writing lane passes fence.proxy.async, its warp meets,
+//             and only then does one lane arrive, so the tile is visible to that
+//             SM's tensor core before the leader can learn of it;
+//   accempty  an accumulator is read (wait::ld) and handed back in one SM's tensor
+//             memory; tcgen05.fence::before_thread_sync orders it before the arrival.
+// A release at cluster scope on ready waits about 1300 clocks a stage for nothing:
+// 2B down projection's dX 92 -> 134 us, 70B-class layer with 128 tokens 52 -> 75, 2B
+// up projection's fp32 dW 182 -> 216, 4-bit-activation layer's bf16 dW 133 -> 178.
+//
 // What bounds it.  Per 64 rows of the sum and CTA, at BN = 256: 512 clocks of
 // tensor work a term, against what passes through 128 bytes a clock of shared
 // memory: A written and read (32 KB a term), dY in and read (32 KB, the read once
@@ -184,27 +198,16 @@ __device__ __forceinline__ void mma_bf16_tile_pair(uint32_t d_tmem, uint32_t a_l
 }
 
 // Whether the phase has completed, without waiting for it.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
-}
-
-// Arrive on CTA 0's copy of a barrier after generic shared-memory writes that
-// the tensor cores read: every writer has passed fence.proxy.async and the
-// warp has met.
-__device__ __forceinline__ void gt_arrive_leader(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .b32 ra;\n\t"
-      "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-      "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -390,7 +393,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       const int r0 = w.rt * BN + static_cast<int>(rank) * C::kHalf;
       for (int c = w.c0; c < w.c1; ++c, ++g) {
         if (g >= static_cast<uint32_t>(S) &&
-            !__all_sync(0xffffffffu, mbar_wait(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty))) {
+            !__all_sync(0xffffffffu,
+                        mbar_wait_cluster(&done[s], ((g / S) & 1) ^ 1u, abort_flag, limit_ns, kSiteProdEmpty))) {
           stop = true;
           break;
         }
@@ -436,7 +440,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           // (every decision to give up is taken by the whole warp: elect.sync
           // below names all its lanes)
           if (i >= 2 &&
-              !__all_sync(0xffffffffu, mbar_wait(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc))) {
+              !__all_sync(0xffffffffu,
+                          mbar_wait_cluster(&accempty[b], ((i >> 1) & 1) ^ 1u, abort_flag, limit_ns, kSiteAcc))) {
             stop = true;
             break;
           }
@@ -444,7 +449,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           const uint32_t d_tmem = tmem + b * BN;
           uint32_t acc = 0;
           for (; c0 < ce; ++c0) {
-            if (!__all_sync(0xffffffffu, seen || mbar_wait(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull))) {
+            if (!__all_sync(0xffffffffu,
+                            seen || mbar_wait_cluster(&ready[s], ph, abort_flag, limit_ns, kSiteMmaExfull))) {
               stop = true;
               break;
             }
@@ -453,7 +459,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
             // this stage's MMAs are issued (a look that succeeds takes 165
             // clocks beside the converters' shared-memory traffic)
             const int sn = s + 1 == S ? 0 : s + 1;
-            seen = mbar_test_wait(&ready[sn], sn ? ph : ph ^ 1u);
+            seen = mbar_test_wait_cluster(&ready[sn], sn ? ph : ph ^ 1u);
             if (elect_one()) {
               const uint32_t alo = a0 + as * (C::kASlotBytes / 16), blo = b0 + s * (C::kInBytes / 16);
 #pragma unroll
@@ -503,7 +509,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           bool ok = true;
           if (g >= static_cast<uint32_t>(C::kASlots)) {
             const uint32_t gp = g - C::kASlots;
-            ok = mbar_wait(&done[gp % S], (gp / S) & 1, abort_flag, limit_ns, kSiteExpEmpty);
+            ok = mbar_wait_cluster(&done[gp % S], (gp / S) & 1, abort_flag, limit_ns, kSiteExpEmpty);
           }
           ok = ok && mbar_wait(&full[s], (g / S) & 1, abort_flag, limit_ns, kSiteExpFull);
           return __all_sync(0xffffffffu, ok) != 0;
@@ -565,9 +571,9 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
             if (TERMS == 2) st_shared_v4(at + C::kTileBytes, lo[0], lo[1], lo[2], lo[3]);
           }
         }
-        fence_proxy_async_smem();
+        fence_proxy_async_smem();   // every writer, before the warp meets and one lane arrives
         __syncwarp();
-        if (lane == 0) gt_arrive_leader(&ready[s]);
+        if (lane == 0) mbar_arrive_cluster_relaxed(&ready[s], 0);
       }
     }
   } else {
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t*>(P.out) +
                                                         static_cast<size_t>(r0 + t) * P.K + kw));
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (i >> 1) & 1, abort_flag, limit_ns, kSiteAcc) &&
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&accfull[b], (i >> 1) & 1, abort_flag, limit_ns, kSiteAcc) &&
                                        !*abort_flag))
         break;
       tc_fence_after();
@@ -690,7 +696,7 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) gt_arrive_leader(&accempty[b]);   // accumulator drained
+      if (lane == 0) mbar_arrive_cluster_relaxed(&accempty[b], 0);   // accumulator drained
       w.c0 += min(C::kSegment, w.c1 - w.c0);
       fresh = false;
     }
