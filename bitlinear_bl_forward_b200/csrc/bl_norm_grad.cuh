@@ -27,6 +27,7 @@
 
 #include "bl_act.cuh"
 #include "bl_common.cuh"
+#include "bl_tc_common.cuh"
 
 namespace bl {
 
@@ -242,9 +243,10 @@ struct NormGradArgs {
 // returned to every thread.  Within a warp each halving step adds one half of
 // the values and hands the other half to the partner lane: N - 1 + 5 - log2 N
 // shuffles instead of 5 N.  One barrier (id `bar`, 32 nw threads); `slot`
-// ([32][N] floats) alternates between two buffers.
+// ([32][N] floats) alternates between two buffers.  The barrier also takes a
+// decision for the group: whether `ok` holds for all its threads.
 template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], float* slot, int w, int nw, int bar) {
+__device__ __forceinline__ bool group_sum(float (&v)[N], float* slot, int w, int nw, int bar, bool ok) {
   const int lane = threadIdx.x & 31;
   int o = 16;
 #pragma unroll
@@ -261,13 +263,14 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* slot, int w, int
   for (int p = 16 / N; p >= 1; p >>= 1) t += __shfl_xor_sync(0xffffffffu, t, p);
   // lane l holds value l / (32 / N)
   if ((lane & (32 / N - 1)) == 0) slot[w * N + lane / (32 / N)] = t;
-  named_bar_sync(bar, 32 * nw);
+  ok = named_bar_and(bar, 32 * nw, ok);
   t = 0.f;
   for (int i = lane / N; i < nw; i += 32 / N) t += slot[i * N + (lane & (N - 1))];
 #pragma unroll
   for (int p = N; p < 32; p <<= 1) t += __shfl_xor_sync(0xffffffffu, t, p);
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t, i);
+  return ok;
 }
 
 // Row gradients, one row a CTA.
@@ -386,7 +389,9 @@ __global__ void __launch_bounds__(G == 2 ? 640 : 512) bl_norm_bwd_kernel(const N
     }
   };
   stats(m0);
-  for (int it = 0, st = 0, ph = 0; m0 < a.M; m0 += step, ++it) {
+  bool ok = true;
+  int it = 0;
+  for (int st = 0, ph = 0; m0 < a.M; m0 += step, ++it) {
     f2 r[R], nm[R];
     float s[NS];
 #pragma unroll
@@ -395,9 +400,9 @@ __global__ void __launch_bounds__(G == 2 ? 640 : 512) bl_norm_bwd_kernel(const N
       nm[q] = f2_both(-mean[q]);
     }
     if (m0 < a.M - step) stats(m0 + step);
-    // a wait that gives up is recorded in the status word; the rows are then
-    // whatever the stage holds
-    mbar_wait(&full[grp][st], ph, nullptr, limit_ns, kSiteNormRows);
+    // a wait that gives up is recorded in the status word, and ends the group's
+    // loop at the barrier below
+    ok = mbar_wait(&full[grp][st], ph, nullptr, limit_ns, kSiteNormRows);
     const uint8_t* rows = my + static_cast<size_t>(st) * R * 2 * row_bytes;
     auto load = [&](int q, int i, f2 (&dy)[4], f2 (&xh)[4]) {
       f2_bf16x8(*reinterpret_cast<const uint4*>(rows + q * row_bytes + 16 * i), dy);
@@ -428,9 +433,10 @@ __global__ void __launch_bounds__(G == 2 ? 640 : 512) bl_norm_bwd_kernel(const N
     }
     // the barrier inside also says that the group has left the stage before
     if (a.dX)
-      group_sum<NS>(s, slots[grp][it & 1], w, nw, 1 + grp);
+      ok = group_sum<NS>(s, slots[grp][it & 1], w, nw, 1 + grp, ok);
     else
-      named_bar_sync(1 + grp, T);
+      ok = named_bar_and(1 + grp, T, ok);
+    if (!ok) break;
     if (it > 0 && tid == 0 && m0 < a.M - (ST - 1) * step) fetch(m0 + (ST - 1) * step, st == 0 ? ST - 1 : st - 1);
     if (++st == ST) {
       st = 0;
@@ -452,6 +458,16 @@ __global__ void __launch_bounds__(G == 2 ? 640 : 512) bl_norm_bwd_kernel(const N
         }
       }
     }
+  }
+  if (!ok) {
+    // the column sums are not numbers then, and no copy of this group is in flight
+    // when the CTA ends: rows were fetched for the steps up to it + ST - 2 (the first
+    // ST before any step)
+#pragma unroll
+    for (int e = 0; e < 4 * C; ++e) dw[e] = db[e] = f2_both(__int_as_float(0x7FFFFFFF));
+    if (tid == 0)
+      for (int i = it, m = m0; i < (it ? it + ST - 1 : ST) && m < a.M; ++i, m += step)
+        mbar_wait(&full[grp][i % ST], (i / ST) & 1, nullptr, limit_ns, kSiteDrain);
   }
   pdl_launch_dependents();
   if (G == 2) {
