@@ -36,6 +36,7 @@ namespace {
 constexpr int kVersion = 100;                       // 0.1.0
 constexpr int64_t kMaxK = 65536;
 constexpr int64_t kMaxElems = int64_t(1) << 40;     // N*K and M*K bound
+constexpr int64_t kMaxDim = int64_t(INT32_MAX) - 65536;   // leaves 32-bit tile and row counters room past the end
 constexpr int kGemvMaxM = 2;
 constexpr int kAbsumMaxBlocks = 592;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s per wait
@@ -53,10 +54,18 @@ struct NvtxRange {
 };
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-bl_status check_shape_nk(int64_t N, int64_t K) {
+// A weight matrix that is gone over element by element.
+bl_status check_weights_nk(int64_t N, int64_t K) {
   if (N <= 0 || K <= 0 || (K % 64) != 0 || K > kMaxK) return BL_ERR_SHAPE;
   if (N >= kMaxElems / K) return BL_ERR_SHAPE;
   return BL_OK;
+}
+
+// A layer: the kernels count its rows and tiles in 32 bits.
+bl_status check_shape_nk(int64_t N, int64_t K) {
+  bl_status st = check_weights_nk(N, K);
+  if (st != BL_OK) return st;
+  return N > kMaxDim ? BL_ERR_SHAPE : BL_OK;
 }
 
 bl_status check_m(int64_t M, int64_t K) {
@@ -788,7 +797,7 @@ const char* bl_status_string(bl_status s) {
   switch (s) {
     case BL_OK: return "ok";
     case BL_ERR_INVALID_ARG: return "invalid argument (null pointer)";
-    case BL_ERR_SHAPE: return "unsupported shape (need N,K > 0, K % 64 == 0, K <= 65536, M >= 0, N*K < 2^40)";
+    case BL_ERR_SHAPE: return "unsupported shape (need N,K > 0, K % 64 == 0, K <= 65536, M >= 0, N*K < 2^40, N < 2^31 - 65536)";
     case BL_ERR_ALIGNMENT: return "pointer not 16-byte aligned";
     case BL_ERR_UNSUPPORTED: return "unsupported activation width (bits must be 4 or 8)";
     case BL_ERR_CUDA: return "CUDA error";
@@ -816,14 +825,14 @@ static int absum_blocks(int64_t N, int64_t K) {
 }
 
 size_t bl_quantize_weights_workspace_bytes(int64_t N, int64_t K) {
-  if (check_shape_nk(N, K) != BL_OK) return 0;
+  if (check_weights_nk(N, K) != BL_OK) return 0;
   return static_cast<size_t>(bl::kAbsumTotals) * sizeof(unsigned long long);
 }
 
 bl_status bl_quantize_weights(const float* W, int64_t N, int64_t K, uint8_t* Wp, float* gamma, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
   const NvtxRange nvtx_range("bl_quantize_weights");
-  bl_status st = check_shape_nk(N, K);
+  bl_status st = check_weights_nk(N, K);
   if (st != BL_OK) return st;
   if (!W || !Wp || !gamma) return BL_ERR_INVALID_ARG;
   if (!aligned16(W) || !aligned16(Wp)) return BL_ERR_ALIGNMENT;
@@ -847,7 +856,7 @@ bl_status bl_quantize_weights(const float* W, int64_t N, int64_t K, uint8_t* Wp,
 
 bl_status bl_unpack_weights(const uint8_t* Wp, int64_t N, int64_t K, int8_t* codes, cudaStream_t stream) {
   const NvtxRange nvtx_range("bl_unpack_weights");
-  bl_status st = check_shape_nk(N, K);
+  bl_status st = check_weights_nk(N, K);
   if (st != BL_OK) return st;
   if (!Wp || !codes) return BL_ERR_INVALID_ARG;
   if (!aligned16(Wp) || !aligned16(codes)) return BL_ERR_ALIGNMENT;
@@ -1606,13 +1615,11 @@ bl_status check_rows(int64_t M, int64_t K) {
   return check_m(M, K);
 }
 
-// N*K, M*K and M*N below 2^40; M and N leave 32-bit tile and row counters room
-// to step past the end.
+// N*K, M*K and M*N below 2^40; M and N at most kMaxDim.
 bl_status check_mnk(int64_t M, int64_t N, int64_t K) {
-  constexpr int64_t kMaxDim = int64_t(INT32_MAX) - 65536;
   bl_status st = check_shape_nk(N, K);
   if (st != BL_OK) return st;
-  if (N > kMaxDim || M > kMaxDim) return BL_ERR_SHAPE;
+  if (M > kMaxDim) return BL_ERR_SHAPE;
   if ((st = check_m(M, K)) != BL_OK) return st;
   if (M > 0 && M >= kMaxElems / N) return BL_ERR_SHAPE;
   return BL_OK;
@@ -1955,7 +1962,7 @@ extern "C" {
 
 size_t bl_forward_checkpoint_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits) {
   (void)bits;
-  if (check_shape_nk(N, K) != BL_OK || check_m(M, K) != BL_OK) return 0;
+  if (check_mnk(M, N, K) != BL_OK) return 0;
   return align_up(static_cast<size_t>(M) * 4, 256);
 }
 
@@ -1964,9 +1971,8 @@ bl_status bl_forward_checkpoint(const uint16_t* X, int norm, float eps, int64_t 
                                 float* scale, float* stat, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream) {
   const NvtxRange nvtx_range("bl_forward_checkpoint");
-  bl_status st = check_shape_nk(N, K);
+  bl_status st = check_mnk(M, N, K);
   if (st != BL_OK) return st;
-  if ((st = check_m(M, K)) != BL_OK) return st;
   if (bits != 8 && bits != 4) return BL_ERR_UNSUPPORTED;
   if (norm != BL_NORM_NONE && norm != BL_NORM_RMS && norm != BL_NORM_LAYER) return BL_ERR_UNSUPPORTED;
   if (norm != BL_NORM_NONE && !rms_eps_ok(eps)) return BL_ERR_INVALID_ARG;

@@ -51,7 +51,8 @@ extern "C" {
 typedef enum {
   BL_OK = 0,
   BL_ERR_INVALID_ARG = 1, /* null pointer where a tensor is required */
-  BL_ERR_SHAPE = 2,       /* M < 0, N or K <= 0, K % 64 != 0, K > 65536, N*K >= 2^40 */
+  BL_ERR_SHAPE = 2,       /* M < 0, N or K <= 0, K % 64 != 0, K > 65536, N*K >= 2^40; N >= 2^31 - 65536
+                             (but for bl_quantize_weights and bl_unpack_weights) */
   BL_ERR_ALIGNMENT = 3,   /* a pointer that must be 16-byte aligned is not */
   BL_ERR_UNSUPPORTED = 4, /* bits not in {4, 8} */
   BL_ERR_CUDA = 5,        /* a CUDA runtime/driver call failed */
@@ -441,7 +442,8 @@ BL_API bl_status bl_forward_norm_grouped(int count, const bl_linear* problems, i
  *                   of every token; not written, and may be NULL, without a norm
  * bits = 4 codes are stored one a byte.  eps is ignored without a norm.
  * workspace: bl_forward_checkpoint_workspace_bytes(M, K, N, bits) bytes,
- * 16-byte aligned.  The ordering rule of bl_forward applies.
+ * 16-byte aligned.  Shapes as in bl_backward_input.  The ordering rule of
+ * bl_forward applies.
  */
 #define BL_NORM_NONE 2
 BL_API size_t bl_forward_checkpoint_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits);
