@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 
@@ -1601,14 +1602,32 @@ namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Whether [a, a + na) and [b, b + nb) share a byte (null ranges do not).
+// Whether [a, a + na) and [b, b + nb) share a byte (null and empty ranges do not).
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b) return false;
+  if (!a || !b || !na || !nb) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
-// As above, but the same range is fine (a row is read before it is written).
-bool overlaps_partly(const void* a, const void* b, size_t n) { return a != b && overlaps(a, n, b, n); }
+
+// A call's argument as a range of memory (null: not given).  The first output may be
+// exactly an input that is marked so (a row is read before it is written).
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool in_place = false;
+};
+
+// Whether an output (the workspace is one) shares a byte with an input or with
+// another output.
+bool outputs_clash(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+  for (const Span* o = out.begin(); o != out.end(); ++o) {
+    for (const Span& i : in)
+      if (overlaps(o->p, o->bytes, i.p, i.bytes) && !(i.in_place && o == out.begin() && o->p == i.p)) return true;
+    for (const Span* q = o + 1; q != out.end(); ++q)
+      if (overlaps(o->p, o->bytes, q->p, q->bytes)) return true;
+  }
+  return false;
+}
 
 bl_status check_rows(int64_t M, int64_t K) {
   if (K <= 0 || (K % 64) != 0 || K > kMaxK) return BL_ERR_SHAPE;
@@ -1982,9 +2001,13 @@ bl_status bl_forward_checkpoint(const uint16_t* X, int norm, float eps, int64_t 
     return BL_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < bl_forward_checkpoint_workspace_bytes(M, K, N, bits)) return BL_ERR_WORKSPACE;
   if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
-  const size_t x_bytes = static_cast<size_t>(M) * K * 2, q_bytes = static_cast<size_t>(M) * K;
-  const size_t y_bytes = static_cast<size_t>(M) * N * 2;
-  if (overlaps(Y, y_bytes, X, x_bytes) || overlaps(Xq, q_bytes, X, x_bytes) || overlaps(Y, y_bytes, Xq, q_bytes))
+  const size_t rows = static_cast<size_t>(M), codes = rows * K;
+  if (outputs_clash({{Y, rows * N * 2},
+                     {Xq, codes},
+                     {scale, rows * 4},
+                     {norm != BL_NORM_NONE ? stat : nullptr, rows * 4},
+                     {workspace, bl_forward_checkpoint_workspace_bytes(M, K, N, bits)}},
+                    {{X, codes * 2}, {Wp, static_cast<size_t>(N) * K / 4}, {gamma, 4}}))
     return BL_ERR_INVALID_ARG;
   const int Q = bits == 8 ? 127 : 7;
   const int m = static_cast<int>(M), k = static_cast<int>(K);
@@ -2019,9 +2042,9 @@ bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int64_t N,
     if (!workspace || workspace_bytes < need) return BL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
   }
-  const size_t dx_bytes = static_cast<size_t>(M) * K * 2;
-  if (overlaps(dX, dx_bytes, dY, static_cast<size_t>(M) * N * 2) ||
-      overlaps(dX, dx_bytes, Wp, static_cast<size_t>(N) * K / 4))
+  const size_t rows = static_cast<size_t>(M);
+  if (outputs_clash({{dX, rows * K * 2}, {workspace, need}},
+                    {{dY, rows * N * 2}, {Wp, static_cast<size_t>(N) * K / 4}, {gamma, 4}}))
     return BL_ERR_INVALID_ARG;
   bl::GradArgs a = {};
   a.dY = dY;
@@ -2062,8 +2085,9 @@ bl_status bl_backward_weight(const uint16_t* dY, const int8_t* Xq, const float* 
     if (!workspace || workspace_bytes < need) return BL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
   }
-  const size_t dw_bytes = static_cast<size_t>(N) * K * ((flags & BL_GRAD_BF16) ? 2 : 4);
-  if (overlaps(dW, dw_bytes, dY, static_cast<size_t>(M) * N * 2) || overlaps(dW, dw_bytes, Xq, static_cast<size_t>(M) * K))
+  const size_t rows = static_cast<size_t>(M);
+  if (outputs_clash({{dW, static_cast<size_t>(N) * K * ((flags & BL_GRAD_BF16) ? 2 : 4)}, {workspace, need}},
+                    {{dY, rows * N * 2}, {Xq, rows * K}, {scale, rows * 4}}))
     return BL_ERR_INVALID_ARG;
   bl::GradArgs a = {};
   a.dY = dY;
@@ -2089,7 +2113,10 @@ bl_status bl_norm_forward(const uint16_t* X, const uint16_t* weight, const uint1
   if (!X || !Y) return BL_ERR_INVALID_ARG;
   if (!aligned16(X) || !aligned16(Y) || !aligned16(weight) || !aligned16(bias) || !aligned4(mean) || !aligned4(stat))
     return BL_ERR_ALIGNMENT;
-  if (overlaps_partly(X, Y, static_cast<size_t>(M) * K * 2)) return BL_ERR_INVALID_ARG;
+  const size_t rows = static_cast<size_t>(M), vec = static_cast<size_t>(K) * 2;
+  if (outputs_clash({{Y, rows * vec}, {mean, rows * 4}, {stat, rows * 4}},
+                    {{X, rows * vec, true}, {weight, vec}, {bias, vec}}))
+    return BL_ERR_INVALID_ARG;
   const int m = static_cast<int>(M), k = static_cast<int>(K);
   if (norm == BL_NORM_LAYER) return launch_norm_fwd<true>(X, weight, bias, eps, m, k, Y, mean, stat, stream);
   return launch_norm_fwd<false>(X, weight, bias, eps, m, k, Y, nullptr, stat, stream);
@@ -2125,8 +2152,12 @@ bl_status bl_norm_backward(const uint16_t* dY, const uint16_t* X, const uint16_t
     if (!workspace || workspace_bytes < bl_norm_backward_workspace_bytes(M, K)) return BL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return BL_ERR_ALIGNMENT;
   }
-  const size_t row_bytes = static_cast<size_t>(M) * K * 2, w_bytes = static_cast<size_t>(K) * sizeof(float);
-  if (overlaps_partly(dX, dY, row_bytes) || overlaps_partly(dX, X, row_bytes) || overlaps(dweight, w_bytes, dbias, w_bytes))
+  const size_t rows = static_cast<size_t>(M), vec = static_cast<size_t>(K) * 2;
+  if (outputs_clash({{dX, rows * vec},
+                     {dweight, 2 * vec},
+                     {dbias, 2 * vec},
+                     {dweight || dbias ? workspace : nullptr, bl_norm_backward_workspace_bytes(M, K)}},
+                    {{dY, rows * vec, true}, {X, rows * vec, true}, {weight, vec}, {mean, rows * 4}, {stat, rows * 4}}))
     return BL_ERR_INVALID_ARG;
   bl::NormGradArgs a = {};
   a.dY = dY;
@@ -2154,8 +2185,8 @@ bl_status bl_norm_backward_checkpoint(const uint16_t* dXn, const int8_t* Xq, con
   if (!dXn || !Xq || !scale || !stat || !dX) return BL_ERR_INVALID_ARG;
   if (!aligned16(dXn) || !aligned16(Xq) || !aligned16(dX) || !aligned4(scale) || !aligned4(stat))
     return BL_ERR_ALIGNMENT;
-  const size_t row_bytes = static_cast<size_t>(M) * K * 2;
-  if (overlaps_partly(dX, dXn, row_bytes) || overlaps(dX, row_bytes, Xq, static_cast<size_t>(M) * K))
+  const size_t rows = static_cast<size_t>(M), codes = rows * K;
+  if (outputs_clash({{dX, codes * 2}}, {{dXn, codes * 2, true}, {Xq, codes}, {scale, rows * 4}, {stat, rows * 4}}))
     return BL_ERR_INVALID_ARG;
   bl::NormGradArgs a = {};
   a.dY = dXn;

@@ -50,7 +50,7 @@ extern "C" {
 
 typedef enum {
   BL_OK = 0,
-  BL_ERR_INVALID_ARG = 1, /* null pointer where a tensor is required */
+  BL_ERR_INVALID_ARG = 1, /* null pointer where a tensor is required; training calls: ranges that overlap */
   BL_ERR_SHAPE = 2,       /* M < 0, N or K <= 0, K % 64 != 0, K > 65536, N*K >= 2^40; N >= 2^31 - 65536
                              (but for bl_quantize_weights and bl_unpack_weights) */
   BL_ERR_ALIGNMENT = 3,   /* a pointer that must be 16-byte aligned is not */
@@ -427,8 +427,9 @@ BL_API bl_status bl_forward_norm_grouped(int count, const bl_linear* problems, i
  * bf16 activations, and it is exactly what the forward multiplied.
  * A NaN or Inf dY[m,n] makes row m of dX and row n of dW not finite (Inf or NaN),
  * and changes nothing else.
- * Outputs that overlap an input return BL_ERR_INVALID_ARG, but for the rows that
- * a norm may take in place (exactly the same range).  A workspace is clobbered:
+ * An output or workspace that overlaps an input or another output returns
+ * BL_ERR_INVALID_ARG, but for the rows that a norm may take in place (exactly the
+ * same range).  A workspace is clobbered:
  * calls that may overlap on the GPU (streams, graphs replayed at once) need one
  * each.  Outputs are written after the kernels before the call on its stream.
  * ------------------------------------------------------------------------- */
