@@ -644,14 +644,17 @@ def _stream_of(dev: int) -> int:
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _ws_args(workspace, need: int, device):
-    """(pointer, bytes, tensor kept alive) of a caller's or a new workspace."""
+def _ws_args(workspace, need: int, device, dev: int):
+    """(pointer, bytes, tensor kept alive) of a caller's or a new workspace, on
+    device `dev`."""
     if workspace is None:
         if need == 0:
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         _dev(workspace, torch.uint8, "workspace")
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on the current device")
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
@@ -675,7 +678,7 @@ def bl_forward_checkpoint(X: torch.Tensor, Wp: torch.Tensor, gamma: torch.Tensor
     Xq = torch.empty(M, K, dtype=torch.int8, device=X.device)
     scale = torch.empty(M, dtype=torch.float32, device=X.device)
     stat = torch.empty(M, dtype=torch.float32, device=X.device) if nrm != BL_NORM_NONE else None
-    wp, wn, _keep = _ws_args(workspace, lib().bl_forward_checkpoint_workspace_bytes(M, K, N, bits), X.device)
+    wp, wn, _keep = _ws_args(workspace, lib().bl_forward_checkpoint_workspace_bytes(M, K, N, bits), X.device, dev)
     _check(lib().bl_forward_checkpoint(px, nrm, eps, M, K, N, pw, pg, bits, py, Xq.data_ptr(), scale.data_ptr(),
                                        stat.data_ptr() if stat is not None else None, wp, wn, _stream_of(dev)),
            "bl_forward_checkpoint")
@@ -695,7 +698,7 @@ def bl_backward_input(dY: torch.Tensor, Wp: torch.Tensor, gamma: torch.Tensor, K
     pg = _scalar(gamma, "gamma", dev)
     dX = out if out is not None else dY.new_empty(M, K)
     px = dX.data_ptr() if out is None else _train(dX, torch.bfloat16, "out", (M, K), dev)
-    wp, wn, _keep = _ws_args(workspace, lib().bl_backward_input_workspace_bytes(M, K, N), dY.device)
+    wp, wn, _keep = _ws_args(workspace, lib().bl_backward_input_workspace_bytes(M, K, N), dY.device, dev)
     _check(lib().bl_backward_input(py, M, K, N, pw, pg, px, wp, wn, _stream_of(dev)), "bl_backward_input")
     return dX
 
@@ -725,7 +728,7 @@ def bl_backward_weight(dY: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, 
     else:
         po = _train(out, out.dtype, "out", (N, K), dev)
     flags = (BL_GRAD_ACCUMULATE if accumulate else 0) | (BL_GRAD_BF16 if out.dtype == torch.bfloat16 else 0)
-    wp, wn, _keep = _ws_args(workspace, lib().bl_backward_weight_workspace_bytes(M, K, N, flags), dY.device)
+    wp, wn, _keep = _ws_args(workspace, lib().bl_backward_weight_workspace_bytes(M, K, N, flags), dY.device, dev)
     _check(lib().bl_backward_weight(py, pq, ps, M, K, N, flags, po, wp, wn, _stream_of(dev)), "bl_backward_weight")
     return out
 
@@ -775,7 +778,7 @@ def bl_norm_backward(dY: torch.Tensor, X: torch.Tensor, norm: int, stat: torch.T
     pdx = dX.data_ptr() if out is None else _train(dX, torch.bfloat16, "out", (M, K), dev)
     wp, wn, _keep = None, 0, None
     if pdw is not None or pdb is not None:
-        wp, wn, _keep = _ws_args(workspace, lib().bl_norm_backward_workspace_bytes(M, K), X.device)
+        wp, wn, _keep = _ws_args(workspace, lib().bl_norm_backward_workspace_bytes(M, K), X.device, dev)
     _check(lib().bl_norm_backward(py, px, pw, norm, eps, pmu, pst, M, K, BL_GRAD_ACCUMULATE if accumulate else 0, pdx,
                                   pdw, pdb, wp, wn, _stream_of(dev)), "bl_norm_backward")
     return dX, dweight, dbias
