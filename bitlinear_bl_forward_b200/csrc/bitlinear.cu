@@ -1651,7 +1651,8 @@ struct GradPlan {
   int kt, rt;            // tiles along k and r
   bl::GtCut cut;         // chunks of the tiles' sums
   int parts;             // most parts of a tile (1: written directly)
-  int part_row;          // first output row with parts
+  int part_rows, part_cols;   // a part: the tile, or as much of it as there is
+  int places;            // parts that there is room for
   int64_t ld;            // row stride of dY in elements (N, or a padded copy's)
   size_t pad_bytes, part_bytes;
 };
@@ -1702,6 +1703,7 @@ GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N, bool bf16_out) {
       g.cut.nkv = static_cast<int>(nkv);
       g.cut.per = static_cast<int>(per);
       g.cut.chunks = static_cast<int>(chunks);
+      g.cut.over = nkv % per != 0;
       g.parts = static_cast<int>(parts);
     };
     consider(tiles, nk, nk, tiles, 1, ((tiles + P - 1) / P) * std::max(nk * stage, epi) + epi);
@@ -1735,8 +1737,14 @@ GradPlan plan_grad(int kind, int64_t M, int64_t K, int64_t N, bool bf16_out) {
   g.kt = static_cast<int>(kt);
   g.ld = static_cast<int64_t>(align_up(static_cast<size_t>(N), 8));
   g.pad_bytes = g.ld == N ? 0 : align_up(static_cast<size_t>(M) * g.ld * 2, 256);
-  g.part_row = g.cut.whole / static_cast<int>(kt) * g.bn;
-  g.part_bytes = g.parts > 1 ? static_cast<size_t>(g.parts) * (R - g.part_row) * K * sizeof(float) : 0;
+  // room for the parts of the tiles that have some, not for whole rows of tiles: at
+  // most 38 MB where stages are dealt out
+  const int rest = g.kt * g.rt - g.cut.whole;
+  const int first_row = g.cut.whole / g.kt;   // of tiles
+  g.part_rows = first_row < g.rt - 1 ? g.bn : static_cast<int>(R - static_cast<int64_t>(g.rt - 1) * g.bn);
+  g.part_cols = g.kt == 1 ? static_cast<int>(K) : 2 * bl::kGtK;
+  g.places = g.parts > 1 ? g.cut.place(rest - 1, g.cut.chunks - g.cut.whole - 1) + 1 : 0;
+  g.part_bytes = static_cast<size_t>(g.places) * g.part_rows * g.part_cols * sizeof(float);
   return g;
 }
 
@@ -1772,7 +1780,6 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
   P.rt = g.rt;
   P.cut = g.cut;
   P.out = a.out;
-  P.part_row = g.part_row;
   P.accumulate = a.accumulate;
   const bool ok =
       (KIND == bl::kGradInput ? encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, N, K / 4, K / 4, C::kBC,
@@ -1783,10 +1790,10 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
                 KIND == bl::kGradInput ? C::kHalf : C::kBC, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return BL_ERR_CUDA;
   // output tiles, clipped at the last row: of the result, and of the fp32 parts
-  auto encode_out = [&](CUtensorMap* tm, void* base, bool bf16, cuuint64_t rows, cuuint64_t planes) {
+  auto encode_out = [&](CUtensorMap* tm, void* base, bool bf16, cuuint64_t cols, cuuint64_t rows, cuuint64_t planes) {
     EncodeTiledFn enc = get_encode();
-    const cuuint64_t rs = K * (bf16 ? 2 : 4);
-    const cuuint64_t dims[3] = {K, rows, planes};
+    const cuuint64_t rs = cols * (bf16 ? 2 : 4);
+    const cuuint64_t dims[3] = {cols, rows, planes};
     const cuuint64_t strides[2] = {rs, rs * rows};
     const cuuint32_t box[3] = {32, bf16 ? static_cast<cuuint32_t>(C::kChunk) : 16, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
@@ -1794,9 +1801,9 @@ bl_status launch_grad_t(const bl::GradArgs& a, const GradPlan& g, const uint16_t
                       strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                       CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  if (!encode_out(&tmD, a.out, a.out_bf16 != 0, P.R, 1)) return BL_ERR_CUDA;
+  if (!encode_out(&tmD, a.out, a.out_bf16 != 0, K, P.R, 1)) return BL_ERR_CUDA;
   tmP = tmD;   // not used without parts
-  if (g.parts > 1 && !encode_out(&tmP, parts, false, P.R - g.part_row, g.parts)) return BL_ERR_CUDA;
+  if (g.parts > 1 && !encode_out(&tmP, parts, false, g.part_cols, g.part_rows, g.places)) return BL_ERR_CUDA;
   static std::atomic<int> pairs[kMaxDevices];
   int npairs = max_active_pairs(kern, C::kThreads, C::kSmemBytes, pairs);
   if (npairs <= 0) return BL_ERR_CUDA;
@@ -1864,7 +1871,7 @@ bl_status launch_grad(const bl::GradArgs& a, void* workspace, cudaStream_t strea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, bl::bl_grad_join_kernel, static_cast<const float*>(parts), g.cut, g.bn, g.kt,
-                         KIND == bl::kGradInput ? a.M : a.N, a.K, g.part_row, a.gamma, a.out, a.out_bf16,
+                         KIND == bl::kGradInput ? a.M : a.N, a.K, g.part_rows, g.part_cols, a.gamma, a.out, a.out_bf16,
                          a.accumulate) != cudaSuccess)
     return BL_ERR_CUDA;
   return last_cuda();

@@ -126,14 +126,17 @@ struct GtCfg {
 // How the tiles' sums are cut into the chunks that pairs take.  The first `whole`
 // chunks are a tile each, written directly.  The stages of the other tiles (nkv a
 // tile, in a row) are cut into chunks of `per`: a chunk is a part of a tile or runs
-// from one tile into the next ones; what it has of a tile goes to fp32 part
-// chunk - (the tile's first chunk), and the tile's parts are added in that order.
+// from one tile into the next ones; what it has of a tile goes to an fp32 part of
+// the tile's shape, and the tile's parts are added in the order of their chunks.
 // nkv may be above the tile's own stages, so that chunks end with the tile.
 struct GtCut {
   int whole, nkv, per, chunks;
-  // of tile whole + t
+  int over;   // 1: chunks may run over a tile's end (a tile and the next one have parts of the same chunk)
+  // of tile whole + t: its first chunk behind the whole tiles, how many it has, and
+  // where chunk c's part lies (every part has a place of its own)
   __host__ __device__ int first(int t) const { return t * nkv / per; }
   __host__ __device__ int parts(int t) const { return ((t + 1) * nkv - 1) / per - first(t) + 1; }
+  __host__ __device__ int place(int t, int c) const { return c + over * t; }
 };
 
 struct GtArgs {
@@ -143,7 +146,6 @@ struct GtArgs {
   int R, L, K;          // output rows, length of the sum, columns
   int kt, rt;           // tiles along k and r
   GtCut cut;
-  int part_row;         // first output row that has parts: they are fp32 [parts][R - part_row][K]
   int accumulate;       // out += (weight)
 };
 
@@ -341,11 +343,11 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   // The pieces of this pair's chunks, in order: tile (k fastest, so that
-  // neighbouring pairs share a slab of dY), stages [c0, c1) and part (-1: the whole
-  // tile).  Every role walks them by itself.
+  // neighbouring pairs share a slab of dY), stages [c0, c1) and its part's place (-1:
+  // the whole tile).  Every role walks them by itself.
   struct Walk {
     int chunk, u, end;          // next stage of the chunk, its end (parts only)
-    int kt, rt, c0, c1, part;
+    int kt, rt, c0, c1, place;
   };
   auto start = [&]() {
     Walk w;
@@ -365,13 +367,13 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     int tile = w.chunk;
     w.c0 = 0;
     w.c1 = nk;
-    w.part = -1;
+    w.place = -1;
     if (w.chunk >= P.cut.whole) {
       const int t = w.u / P.cut.nkv;
       tile = P.cut.whole + t;
       w.c0 = w.u - t * P.cut.nkv;
       w.c1 = min(nk, w.c0 + w.end - w.u);
-      w.part = w.chunk - P.cut.whole - P.cut.first(t);
+      w.place = P.cut.place(t, w.chunk - P.cut.whole);
       w.u = min(w.end, (t + 1) * P.cut.nkv);
     }
     w.kt = tile % P.kt;
@@ -598,10 +600,11 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
         fresh = true;
       }
       // (two terms: an fp32 result; one: a bf16 one; parts are fp32)
-      const bool direct = w.part < 0, bf16 = TERMS == 1 && direct;
+      const bool direct = w.place < 0, bf16 = TERMS == 1 && direct;
       const bool bf16_acc = KIND == kGradWeight && bf16 && P.accumulate;
       const CUtensorMap* tm = direct ? &tmD : &tmP;
-      const int part = direct ? 0 : w.part, row0 = direct ? 0 : P.part_row;
+      // where the tile's corner lies in what the map covers
+      const int place = direct ? 0 : w.place, row0 = direct ? 0 : w.rt * BN, col0 = direct ? 0 : w.kt * 2 * kGtK;
       const int b = i & 1;
       const int kw = w.kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32;
       const int r0 = w.rt * BN + half * C::kHalf;
@@ -687,9 +690,9 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           __syncwarp();
           if (lane == 0) {
             if (add)
-              tma_reduce_add_3d(tm, kw, r + h - row0, part, tile);
+              tma_reduce_add_3d(tm, kw - col0, r + h - row0, place, tile);
             else
-              tma_store_3d(tm, kw, r + h - row0, part, tile);
+              tma_store_3d(tm, kw - col0, r + h - row0, place, tile);
             bulk_commit_group();
           }
         }
@@ -721,15 +724,17 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
 // parts) take 240 us, 249 with a float4 a thread and an ordinary launch.
 constexpr int kGtJoinRows = 16;
 __global__ void __launch_bounds__(256)
-    bl_grad_join_kernel(const float* __restrict__ part, const GtCut cut, int bn, int kt, int R, int K, int part_row,
-                        const float* __restrict__ gamma, void* __restrict__ out, int out_bf16, int accumulate) {
+    bl_grad_join_kernel(const float* __restrict__ part, const GtCut cut, int bn, int kt, int R, int K, int part_rows,
+                        int part_cols, const float* __restrict__ gamma, void* __restrict__ out, int out_bf16,
+                        int accumulate) {
   pdl_wait();
   const int per_tile = bn / kGtJoinRows, t = blockIdx.x / per_tile;
-  const int tile = cut.whole + t, k = tile % kt * 2 * kGtK + 4 * (threadIdx.x & 63);
-  const int r0 = tile / kt * bn + (blockIdx.x - t * per_tile) * kGtJoinRows + (threadIdx.x >> 6);
+  const int tile = cut.whole + t, kl = 4 * (threadIdx.x & 63), k = tile % kt * 2 * kGtK + kl;
+  const int rl = (blockIdx.x - t * per_tile) * kGtJoinRows + (threadIdx.x >> 6), r0 = tile / kt * bn + rl;
   if (k >= K) return;
   const int parts = cut.parts(t);
-  const size_t plane = static_cast<size_t>(R - part_row) * K;
+  const size_t plane = static_cast<size_t>(part_rows) * part_cols;
+  const float* src = part + cut.place(t, cut.first(t)) * plane + rl * part_cols + kl;
   float4 s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -738,7 +743,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + 4 * i;
-      v[i] = r < R ? __ldcg(reinterpret_cast<const float4*>(part + j * plane + static_cast<size_t>(r - part_row) * K + k))
+      v[i] = r < R ? __ldcg(reinterpret_cast<const float4*>(src + j * plane + 4 * i * part_cols))
                    : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
