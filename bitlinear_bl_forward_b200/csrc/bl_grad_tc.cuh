@@ -558,8 +558,11 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kUnits; ++i) {
             const int row = row0 + i * kRowStep;
+            // within 2^-23, far below the operand's step.  A flushed reciprocal (scales above
+            // 2^126) changes nothing that counts: q / s is no normal bf16 there, and above
+            // 2^110 the lo of an fp32 result is not, which the entry point's limit says.
             float r;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc[i]));   // within 2^-23, far below the operand's step
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc[i]));
             uint64_t rr;
             asm("mov.b64 %0, {%1, %1};" : "=l"(rr) : "f"(r));
             const uint32_t x0 = q[i].x ^ 0x80808080u, x1 = q[i].y ^ 0x80808080u;

@@ -479,9 +479,12 @@ BL_API bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int
  * product at most), a bf16 dW as one bf16 (2^-8, like its own rounding): half
  * the tensor-core work.
  * dY: bf16 bits [M, N], 16-byte aligned.  Xq: int8 [M, K], 16-byte aligned.
- * scale: fp32 [M], positive normal numbers, 4-byte aligned.  dW: 16-byte
- * aligned.  N and limits as in bl_backward_input.  M == 0 writes zeros (nothing with BL_GRAD_ACCUMULATE).  Results do not
- * depend on the run.  workspace: bl_backward_weight_workspace_bytes(M, K, N,
+ * scale: fp32 [M], 4-byte aligned: positive, at most 2^110, and such that |Xq / scale|
+ * is at most the largest bf16.  (The forward writes 2^-125.3 to 2^23.6.  Above 2^110
+ * the second bf16 of Xq / scale leaves the normal numbers, above 2^126 the quotient
+ * itself does: dW is then wrong, up to zero.)  dW: 16-byte aligned.  N and limits as in
+ * bl_backward_input.  M == 0 writes zeros (nothing with BL_GRAD_ACCUMULATE).  Results
+ * do not depend on the run.  workspace: bl_backward_weight_workspace_bytes(M, K, N,
  * flags) bytes (may be 0), 16-byte aligned.
  */
 #define BL_GRAD_ACCUMULATE 1u
