@@ -66,6 +66,7 @@ SIGNATURES = {
     "bl_backward_input": (_int, [_p, _i64, _i64, _i64, _p, _p, _p, _p, _sz, _p]),
     "bl_backward_weight_workspace_bytes": (_sz, [_i64, _i64, _i64, ctypes.c_uint]),
     "bl_backward_weight": (_int, [_p, _p, _p, _i64, _i64, _i64, ctypes.c_uint, _p, _p, _sz, _p]),
+    "bl_gradient_plan": (_int, [_int, _i64, _i64, _i64, ctypes.c_uint, ctypes.POINTER(ctypes.c_int32)]),
     "bl_norm_forward": (_int, [_p, _p, _p, _int, ctypes.c_float, _i64, _i64, _p, _p, _p, _p]),
     "bl_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
     "bl_norm_backward": (_int, [_p, _p, _p, _int, ctypes.c_float, _p, _p, _i64, _i64, ctypes.c_uint, _p, _p, _p, _p,
@@ -731,6 +732,15 @@ def bl_backward_weight(dY: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, 
     wp, wn, _keep = _ws_args(workspace, lib().bl_backward_weight_workspace_bytes(M, K, N, flags), dY.device, dev)
     _check(lib().bl_backward_weight(py, pq, ps, M, K, N, flags, po, wp, wn, _stream_of(dev)), "bl_backward_weight")
     return out
+
+
+def bl_gradient_plan(weight: bool, M: int, K: int, N: int, flags: int = 0):
+    """How a gradient of this shape is cut (test export): (output rows of a tile,
+    tiles, tiles written whole, stages of a tile's sum, stages of a part, most
+    parts of a tile)."""
+    plan = (ctypes.c_int32 * 6)()
+    _check(lib().bl_gradient_plan(int(weight), M, K, N, flags, plan), "bl_gradient_plan")
+    return tuple(plan)
 
 
 def bl_norm_forward(X: torch.Tensor, norm: int, weight: torch.Tensor | None = None,

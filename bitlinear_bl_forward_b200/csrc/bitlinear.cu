@@ -2109,6 +2109,24 @@ bl_status bl_backward_weight(const uint16_t* dY, const int8_t* Xq, const float* 
   return launch_grad<bl::kGradWeight>(a, workspace, stream);
 }
 
+bl_status bl_gradient_plan(int weight, int64_t M, int64_t K, int64_t N, unsigned flags, int32_t plan[6]) {
+  bl_status st = check_mnk(M, N, K);
+  if (st != BL_OK) return st;
+  if (M == 0) return BL_ERR_SHAPE;
+  if ((weight != 0 && weight != 1) || (flags & ~(weight ? BL_GRAD_ACCUMULATE | BL_GRAD_BF16 : 0u)) != 0u)
+    return BL_ERR_UNSUPPORTED;
+  if (!plan) return BL_ERR_INVALID_ARG;
+  const GradPlan g = plan_grad(weight ? bl::kGradWeight : bl::kGradInput, M, K, N, (flags & BL_GRAD_BF16) != 0);
+  const int bc = bl::gt_bc(weight ? bl::kGradWeight : bl::kGradInput, g.bn);
+  plan[0] = g.bn;
+  plan[1] = g.kt * g.rt;
+  plan[2] = g.cut.whole;
+  plan[3] = static_cast<int32_t>(((weight ? M : N) + bc - 1) / bc);
+  plan[4] = g.cut.per;
+  plan[5] = g.parts;
+  return BL_OK;
+}
+
 bl_status bl_norm_forward(const uint16_t* X, const uint16_t* weight, const uint16_t* bias, int norm, float eps,
                           int64_t M, int64_t K, uint16_t* Y, float* mean, float* stat, cudaStream_t stream) {
   const NvtxRange nvtx_range("bl_norm_forward");

@@ -495,6 +495,15 @@ BL_API bl_status bl_backward_weight(const uint16_t* dY, const int8_t* Xq, const 
                                     cudaStream_t stream);
 
 /*
+ * How a gradient of this shape is cut into tiles and parts (for tests; no GPU, and
+ * nothing is launched).  weight: 0 bl_backward_input, 1 bl_backward_weight with these
+ * flags.  plan receives: output rows of a tile (by 256 columns), tiles, tiles that are
+ * summed whole and written directly (the first ones), stages of a tile's sum, stages of
+ * a part, most parts of one tile.
+ */
+BL_API bl_status bl_gradient_plan(int weight, int64_t M, int64_t K, int64_t N, unsigned flags, int32_t plan[6]);
+
+/*
  * RMSNorm (norm == BL_NORM_RMS) or LayerNorm (BL_NORM_LAYER) of bf16 rows as
  * an operator of its own (e.g. before the output head), in fp32:
  *   LAYER: mu = (1/K) sum_k x, stat = (1/K) sum_k (x - mu)^2
