@@ -606,8 +606,6 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
       const bool direct = w.place < 0, bf16 = TERMS == 1 && direct;
       const bool bf16_acc = KIND == kGradWeight && bf16 && P.accumulate;
       const CUtensorMap* tm = direct ? &tmD : &tmP;
-      // where the tile's corner lies in what the map covers
-      const int place = direct ? 0 : w.place, row0 = direct ? 0 : w.rt * BN, col0 = direct ? 0 : w.kt * 2 * kGtK;
       const int b = i & 1;
       const int kw = w.kt * 2 * kGtK + static_cast<int>(rank) * kGtK + q * 32;
       const int r0 = w.rt * BN + half * C::kHalf;
@@ -692,10 +690,13 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
+            // in the result, or in a part of the tile's shape
+            const int x = direct ? kw : kw - w.kt * 2 * kGtK, y = direct ? r + h : r + h - w.rt * BN;
+            const int z = direct ? 0 : w.place;
             if (add)
-              tma_reduce_add_3d(tm, kw - col0, r + h - row0, place, tile);
+              tma_reduce_add_3d(tm, x, y, z, tile);
             else
-              tma_store_3d(tm, kw - col0, r + h - row0, place, tile);
+              tma_store_3d(tm, x, y, z, tile);
             bulk_commit_group();
           }
         }
