@@ -1657,7 +1657,9 @@ struct GradPlan {
   size_t pad_bytes, part_bytes;
 };
 
-constexpr unsigned kGradPlanPairs = 74;   // CTA pairs of a B200
+// CTA pairs of a B200.  Fixed: cuts, and with them the results, do not depend on how
+// many pairs the device at hand runs at once (the chunks are dealt to those there are).
+constexpr unsigned kGradPlanPairs = 74;
 
 // Tiles of 256 k by bn r on 74 CTA pairs, and how their sums are cut: whole
 // tiles; every tile in the same number of parts; or whole waves of whole tiles and

@@ -74,9 +74,11 @@ constexpr int kQSmemBytes = kQEpiOffset + 2 * kQBN * 8 + 1024;
 // time): the branch it guards stays warp-uniform for the compiler, so that
 // descriptors, addresses and coordinates live in uniform registers.  Behind a
 // lane == 0 branch the gradient kernel's four MMAs took 450 clocks to issue and a
-// stage's two TMA loads 490, beside 512 clocks of tensor work; here the 70B-class
-// layer with 2048 tokens went from 320 to 292 us.  A decision to leave a loop is
-// taken by the whole warp: elect.sync names all its lanes.
+// stage's two TMA loads 490, beside 512 clocks of tensor work; here the forward of
+// the 70B-class layer with 2048 tokens (quantiser included) went from 320 to 292 us
+// in runs of some milliseconds, and from 352-356 to 321 us in seconds-long ones under
+// the power cap.  A decision to leave a loop is taken by the whole warp: elect.sync
+// names all its lanes.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(

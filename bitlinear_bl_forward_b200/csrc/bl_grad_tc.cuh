@@ -32,7 +32,9 @@
 // summed in segments of 2048 tokens, which the epilogue adds up with rounding
 // (5.3e-6; a plain fp32 product: 1.1e-6): the pair that owns the tile stores the
 // first segment and adds the others to its own output, which is still in L2.
-// Segments of 1024 tokens cost 3% more.
+// Segments of 1024 tokens cost 3% more.  bf16 results take their whole sum in one
+// accumulator: short by up to 6.3e-9 of itself a term (8.2e-4 over 131072 terms of one
+// sign, 1.4e-4 of mixed signs, where the output's rounding is 1.7e-3 of the norm).
 //
 // Order between the two CTAs.  Waits on barriers that the other CTA's threads or
 // the leader's commits arrive on (ready, done, accfull, accempty) acquire at
@@ -589,7 +591,8 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
     // added to is rounded once: what is there comes into the staging tile 16 bytes a
     // lane, and each lane adds its column.  Output of 8192 x 28672, 16 tokens: fp32 153
     // us stored, 403 added to (4.7 TB/s; 540 with plain loads instead of reductions);
-    // bf16 128 and 274 us (930 with plain loads and stores of 2 bytes a lane).
+    // bf16 128 and 271 us (930 with plain loads and stores of 2 bytes a lane; one
+    // staging tile a warp, so that load, addition and store follow one another).
     const int q = warp & 3, half = (warp - C::kFirstEpi) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float f = P.gamma ? *P.gamma : 1.f;

@@ -16,9 +16,11 @@
 // result does not depend on the run).
 //
 // Bound by the bytes: one read of every input row and one write of every output
-// row.  Measured (B200, 4096 x 2560, rows in HBM): forward 7.1 us, 5.9 TB/s (90%
+// row.  Measured (B200, 4096 x 2560, rows in HBM): forward 7.2 us, 5.8 TB/s (90%
 // of a copy's rate); row gradients alone 10.1 us; with the weight's gradient 13
-// (RMSNorm) to 16 us (LayerNorm) and 4 us for the join, against 9.6 us of bytes.
+// (RMSNorm) to 16.7 us (LayerNorm) and 4 us for the join, against 9.6 us of bytes;
+// from the checkpoint 11.8-12.1 us against 8.0 (one row a CTA: nothing is in flight
+// between a row's sums and the next row's loads).
 // There a group has seven steps, and what comes on top is the first fetch, the merge
 // of the groups and the partial rows: neither fewer instructions a step (rows kept in
 // registers between the passes) nor a hidden barrier (a step's dX behind the next
@@ -32,7 +34,9 @@
 namespace bl {
 
 constexpr unsigned int kSiteNormRows = 8;   // wait-site identifier (see bl_tc_common.cuh)
-constexpr int kNgSms = 148;           // CTAs of the weight gradient's partial rows: a multiple of the SMs
+// CTAs of the weight gradient's partial rows: a multiple of a B200's SMs, fixed, so that
+// the workspace query needs no device and the order of the sums no device's count.
+constexpr int kNgSms = 148;
 constexpr int kNgRowMaxK = 8192;      // widest row whose weight gradient stays in registers
 
 __device__ __forceinline__ float2 warp_sum2(float2 v) {
@@ -513,6 +517,10 @@ __global__ void __launch_bounds__(G == 2 ? 640 : 512) bl_norm_bwd_kernel(const N
 // Row gradients of wide rows, which do not fit the registers: the sums in one
 // pass over the row, dX in a second one (the row is in L2 by then).  A thread
 // reads again only what it will overwrite itself, so dX may be dY or X.
+// With weight gradients, bl_norm_wgrad_cols_kernel reads dY and X once more before.
+// Measured (B200, LayerNorm): 2048 x 28672 73 us for dX, 47 for the columns, 15 for the
+// join (135; 54 of bytes), 4096 x 16384 92 + 52 + 12 (156; 61), 257 x 28672 11 + 9 + 10
+// (30; 6.8).
 template <bool LAYER, bool CKPT>
 __global__ void __launch_bounds__(1024) bl_norm_dx_wide_kernel(const NormGradArgs a) {
   __shared__ float2 slot[32];

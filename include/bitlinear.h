@@ -425,6 +425,14 @@ BL_API bl_status bl_forward_norm_grouped(int count, const bl_linear* problems, i
  * (dW is the gradient of the latent weights W).  What has to be kept between
  * the two passes is M*K bytes of codes and 4*M bytes of scales, half of the
  * bf16 activations, and it is exactly what the forward multiplied.
+ * Precision: gradients between calls are bf16.  The dX of bl_backward_input is rounded
+ * to bf16 before bl_norm_backward_checkpoint reads it, whose dX is rounded once more:
+ * two roundings, 2.3e-3 of the norm apart from 64 bits instead of 1.7e-3.  The tensor
+ * cores truncate when they add to their fp32 sums, so a sum comes out short by up to
+ * 6.3e-9 of itself a term (8.2e-4 over 131072 terms of one sign, 1.4e-4 of mixed signs):
+ * below the half step of a bf16 dX or dW up to half a million terms.  An fp32 dW is
+ * summed 2048 tokens at a time, and rounded to nearest between: 5.5e-6 of the norm at
+ * any number of tokens (8.9e-6 where all products have one sign; 2.6e-6 up to 256).
  * A NaN or Inf dY[m,n] makes row m of dX and row n of dW not finite (Inf or NaN),
  * and changes nothing else.
  * An output or workspace that overlaps an input or another output returns
@@ -512,7 +520,10 @@ BL_API bl_status bl_gradient_plan(int weight, int64_t M, int64_t K, int64_t N, u
  * X, Y: bf16 bits [M, K], 16-byte aligned; Y may be X.  weight, bias: bf16
  * bits [K], 16-byte aligned, or NULL.  mean: fp32 [M] (LAYER; may be NULL,
  * must be NULL for RMS), stat: fp32 [M] or NULL: what bl_norm_backward needs.
- * Unlike the normalising forwards above, the statistics are plain fp32 sums.
+ * Unlike the normalising forwards above, the statistics are plain fp32 sums: the sum
+ * over a row of x, and of the squares that stat averages, have to stay below 2^128
+ * (every |x| below 2^64 / sqrt(K) is enough).  Beyond, stat is Inf and the row's Y zero,
+ * or not a number; other rows are not touched by it.
  * eps positive and finite.  K % 64 == 0.  M == 0 is a no-op.
  */
 BL_API bl_status bl_norm_forward(const uint16_t* X, const uint16_t* weight, const uint16_t* bias, int norm, float eps,

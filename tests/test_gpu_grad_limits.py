@@ -59,3 +59,33 @@ def test_smallest_activations():
     q, s = bl.bl_quant_act(X)
     assert s.item() <= 2.0**23.6
     check(s.item(), q[0], 1.0)
+
+
+@pytest.mark.parametrize("norm", [bl.BL_NORM_RMS, bl.BL_NORM_LAYER])
+@pytest.mark.parametrize("K", [64, 2560, 8256])
+def test_norm_rows_beyond_the_sums_range(K, norm):
+    # squares whose sum passes 2^128 leave an infinite statistic in their row; the
+    # largest row that the limit allows, and every other row, are as without them
+    g = torch.Generator().manual_seed(K)
+    X = torch.randn(6, K, generator=g).to(torch.bfloat16)
+    X[4] = (torch.rand(K, generator=g) - 0.5).to(torch.bfloat16) * (2.0**64 / K**0.5)
+    bad = X.clone()
+    bad[2, K // 2] = 1e30
+    X, bad = X.cuda(), bad.cuda()
+    Y, mean, stat = bl.bl_norm_forward(X, norm)
+    Yb, meanb, statb = bl.bl_norm_forward(bad, norm)
+    others = [0, 1, 3, 4, 5]
+    assert torch.isinf(statb[2]) and torch.isfinite(stat).all() and torch.isfinite(Y.float()).all()
+    assert torch.equal(Y[others], Yb[others]) and torch.equal(stat[others], statb[others])
+    if mean is not None:
+        assert torch.equal(mean[others], meanb[others])
+    # the large row's values: mean 0, statistic far above eps
+    x = X[4].to(F64)
+    d = x - x.mean() if norm == bl.BL_NORM_LAYER else x
+    want = d / d.square().mean().sqrt()
+    # 2^-8 of the output; sums of K fp32 terms, at most K / 32 + 16 additions deep, of
+    # the statistic (half of it in the root) and of the mean; 2^-20 for the rest
+    depth = 2.0**-24 * (K / 32 + 16)
+    spread = x.abs().mean() / d.square().mean().sqrt()
+    tol = (2.0**-8 + depth + 2.0**-20) * want.abs() + depth * spread
+    assert bool(((Y[4].to(F64) - want).abs() <= tol).all())
