@@ -560,9 +560,9 @@ __global__ void __launch_bounds__(GtCfg<KIND, TERMS, BN>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kUnits; ++i) {
             const int row = row0 + i * kRowStep;
-            // within 2^-23, far below the operand's step.  A flushed reciprocal (scales above
-            // 2^126) changes nothing that counts: q / s is no normal bf16 there, and above
-            // 2^110 the lo of an fp32 result is not, which the entry point's limit says.
+            // within 2^-23, far below the operand's step.  Scales above 2^126 would have a
+            // subnormal reciprocal, flushed here; the entry point takes them up to 2^110,
+            // where the lo of an fp32 result still is a normal bf16 or below 2^-16 of q / s.
             float r;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc[i]));
             uint64_t rr;

@@ -34,8 +34,8 @@
 namespace bl {
 
 constexpr unsigned int kSiteNormRows = 8;   // wait-site identifier (see bl_tc_common.cuh)
-// CTAs of the weight gradient's partial rows: a multiple of a B200's SMs, fixed, so that
-// the workspace query needs no device and the order of the sums no device's count.
+// CTAs of the weight gradient's partial rows: a multiple of a B200's SMs.  Fixed, so that
+// the workspace query needs no device and the order of the sums does not depend on one.
 constexpr int kNgSms = 148;
 constexpr int kNgRowMaxK = 8192;      // widest row whose weight gradient stays in registers
 

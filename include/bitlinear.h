@@ -431,7 +431,7 @@ BL_API bl_status bl_forward_norm_grouped(int count, const bl_linear* problems, i
  * cores truncate when they add to their fp32 sums, so a sum comes out short by up to
  * 6.3e-9 of itself a term (8.2e-4 over 131072 terms of one sign, 1.4e-4 of mixed signs):
  * below the half step of a bf16 dX or dW up to half a million terms.  An fp32 dW is
- * summed 2048 tokens at a time, and rounded to nearest between: 5.5e-6 of the norm at
+ * summed 2048 tokens at a time, and rounded to nearest between: about 5.5e-6 of the norm at
  * any number of tokens (8.9e-6 where all products have one sign; 2.6e-6 up to 256).
  * A NaN or Inf dY[m,n] makes row m of dX and row n of dW not finite (Inf or NaN),
  * and changes nothing else.
@@ -489,8 +489,8 @@ BL_API bl_status bl_backward_input(const uint16_t* dY, int64_t M, int64_t K, int
  * dY: bf16 bits [M, N], 16-byte aligned.  Xq: int8 [M, K], 16-byte aligned.
  * scale: fp32 [M], 4-byte aligned: positive, at most 2^110, and such that |Xq / scale|
  * is at most the largest bf16.  (The forward writes 2^-125.3 to 2^23.6.  Above 2^110
- * the second bf16 of Xq / scale leaves the normal numbers, above 2^126 the quotient
- * itself does: dW is then wrong, up to zero.)  dW: 16-byte aligned.  N and limits as in
+ * the second bf16 of Xq / scale leaves the normal numbers, above 2^126 the reciprocal
+ * does and counts as zero: dW is then wrong, up to zero.)  dW: 16-byte aligned.  N and limits as in
  * bl_backward_input.  M == 0 writes zeros (nothing with BL_GRAD_ACCUMULATE).  Results
  * do not depend on the run.  workspace: bl_backward_weight_workspace_bytes(M, K, N,
  * flags) bytes (may be 0), 16-byte aligned.
